@@ -24,16 +24,13 @@
 //      the update.  The blocked order keeps a 10^5-occurrence row
 //      from being one serial chain of 10^5 dependent adds.
 #include "common.hpp"
+#include "radix_sort.hpp"
 
 #include <mutex>
 
 namespace dlrm {
 namespace {
 
-constexpr int RT = 256;                // threads per sort block
-constexpr int ITEMS = 16;              // keys per thread per tile
-constexpr int TILE = RT * ITEMS;       // 4096 positions per tile
-constexpr int kMaxDigits = 512;        // buckets of a digit of at most 9 bits
 constexpr int kHot = 128;              // occurrences from which a segment is "hot", and its block size
 // Persistent blocks of the short-segment kernel and of the hot-run kernels:
 // four and two per CU.  In a training step the update runs beside the MLP
@@ -66,248 +63,6 @@ __global__ __launch_bounds__(256) void build_keys_kernel(const int64_t* __restri
   for (int64_t p = a + gl; p < e; p += G) {
     keys[p] = hi | (uint32_t)idx[p];
     vals[p] = b;
-  }
-}
-
-// ------------------------------------------------------------------ radix sort
-//
-// A pass is four kernels without any waiting between blocks: the per-tile
-// digit counts (tile_hist_kernel, counts[tile][digit]); their sums over
-// chunks of 64 tiles (chunk_sum_kernel); the offsets, each (tile, digit)'s
-// first position = the digit's start (the totals of the digits below it) +
-// the digit's count in earlier chunks + in earlier tiles of its chunk
-// (tile_offset_kernel); and the stable scatter of each tile
-// (scatter_kernel), which ranks its keys with wave ballots and writes them
-// through LDS in digit order, so each digit's keys of a tile leave as one
-// contiguous span.
-constexpr int kChunk = 64;  // tiles per chunk of the offset scan
-
-// block-wide exclusive scan of one value per thread (256 threads); returns
-// the exclusive prefix and writes the block total to *total
-__device__ __forceinline__ uint32_t block_exclusive_scan(uint32_t v, uint32_t* s_wave, uint32_t* total) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  uint32_t x = v;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const uint32_t y = __shfl_up(x, o, 64);
-    if (lane >= o) x += y;
-  }
-  if (lane == 63) s_wave[wave] = x;
-  __syncthreads();
-  uint32_t before = 0, all = 0;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    const uint32_t c = s_wave[w];
-    if (w < wave) before += c;
-    all += c;
-  }
-  __syncthreads();
-  *total = all;
-  return before + x - v;
-}
-
-// Tile t's keys: wave w holds positions w * 1024 + 64 i + lane of the tile
-// (item i), the layout the scatter ranks in.
-__device__ __forceinline__ int tile_pos(int wave, int i, int lane) { return wave * (TILE / 4) + 64 * i + lane; }
-
-// counts[tile][digit] of one pass (per-wave LDS counters).
-template <int DB>
-__global__ __launch_bounds__(RT) void tile_hist_kernel(const uint32_t* __restrict__ keys, int n, int shift,
-                                                       uint32_t* __restrict__ counts, int tiles) {
-  constexpr int NB = 1 << DB;
-  __shared__ uint32_t cnt[4][NB];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  for (int i = tid; i < 4 * NB; i += RT) (&cnt[0][0])[i] = 0u;
-  __syncthreads();
-  const int64_t t0 = (int64_t)blockIdx.x * TILE;
-  const int cnt_n = (int)(n - t0 < TILE ? n - t0 : TILE);
-  uint32_t key[ITEMS];
-#pragma unroll
-  for (int i = 0; i < ITEMS; ++i) {
-    const int q = tile_pos(wave, i, lane);
-    key[i] = q < cnt_n ? keys[t0 + q] : 0u;
-  }
-#pragma unroll
-  for (int i = 0; i < ITEMS; ++i)
-    if (tile_pos(wave, i, lane) < cnt_n) atomicAdd(&cnt[wave][(key[i] >> shift) & (uint32_t)(NB - 1)], 1u);
-  __syncthreads();
-  for (int dg = tid; dg < NB; dg += RT)
-    counts[(int64_t)blockIdx.x * NB + dg] = cnt[0][dg] + cnt[1][dg] + cnt[2][dg] + cnt[3][dg];
-}
-
-// sums[chunk][digit] = the digit's count over the chunk's tiles: block
-// (chunk, 64-digit group), lane = digit, wave w takes 16 of the 64 tiles.
-template <int DB>
-__global__ __launch_bounds__(RT) void chunk_sum_kernel(const uint32_t* __restrict__ counts, int tiles,
-                                                       uint32_t* __restrict__ sums) {
-  constexpr int NB = 1 << DB;
-  __shared__ uint32_t part[4][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int dg = blockIdx.y * 64 + lane;
-  const int t0 = blockIdx.x * kChunk + wave * (kChunk / 4);
-  uint32_t v[kChunk / 4];
-#pragma unroll
-  for (int i = 0; i < kChunk / 4; ++i) v[i] = t0 + i < tiles ? counts[(int64_t)(t0 + i) * NB + dg] : 0u;
-  uint32_t s = 0;
-#pragma unroll
-  for (int i = 0; i < kChunk / 4; ++i) s += v[i];
-  part[wave][lane] = s;
-  __syncthreads();
-  if (wave == 0) sums[(int64_t)blockIdx.x * NB + dg] = part[0][lane] + part[1][lane] + part[2][lane] + part[3][lane];
-}
-
-// sum of col[0], col[stride], ..., col[(rows - 1) stride], eight loads in flight
-__device__ __forceinline__ uint32_t column_sum(const uint32_t* __restrict__ col, int64_t stride, int rows) {
-  uint32_t t = 0;
-  for (int r0 = 0; r0 < rows; r0 += 8) {
-    uint32_t v[8];
-#pragma unroll
-    for (int u = 0; u < 8; ++u) v[u] = r0 + u < rows ? col[(int64_t)(r0 + u) * stride] : 0u;
-#pragma unroll
-    for (int u = 0; u < 8; ++u) t += v[u];
-  }
-  return t;
-}
-
-// offsets[tile][digit] for the tiles of chunk blockIdx.x and the digits of
-// group blockIdx.y: the digit totals (all chunk sums: every block redoes
-// the sums and their exclusive scan over digits), the digit's count in
-// earlier chunks, then in earlier tiles of the chunk (wave w: tiles
-// 16 w .. 16 w + 15, after the three waves before it).
-template <int DB>
-__global__ __launch_bounds__(RT) void tile_offset_kernel(const uint32_t* __restrict__ counts,
-                                                         const uint32_t* __restrict__ sums, int tiles,
-                                                         uint32_t* __restrict__ offsets) {
-  constexpr int NB = 1 << DB, DPT = NB / RT;
-  __shared__ uint32_t s_wave[4];
-  __shared__ uint32_t dstart[NB];
-  __shared__ uint32_t part[4][64];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int chunks = (tiles + kChunk - 1) / kChunk;
-  const int chunk = blockIdx.x;
-  // digit totals and starts (thread: digits DPT tid .. DPT tid + DPT - 1)
-  uint32_t tot[DPT];
-  uint32_t tsum = 0;
-#pragma unroll
-  for (int j = 0; j < DPT; ++j) {
-    tot[j] = column_sum(sums + tid * DPT + j, NB, chunks);
-    tsum += tot[j];
-  }
-  uint32_t total;
-  uint32_t run = block_exclusive_scan(tsum, s_wave, &total);
-#pragma unroll
-  for (int j = 0; j < DPT; ++j) {
-    dstart[tid * DPT + j] = run;
-    run += tot[j];
-  }
-  __syncthreads();
-  const int dg = blockIdx.y * 64 + lane;
-  uint32_t base = dstart[dg] + column_sum(sums + dg, NB, chunk);
-  const int t0 = chunk * kChunk + wave * (kChunk / 4);
-  uint32_t v[kChunk / 4];
-#pragma unroll
-  for (int i = 0; i < kChunk / 4; ++i) v[i] = t0 + i < tiles ? counts[(int64_t)(t0 + i) * NB + dg] : 0u;
-  uint32_t s = 0;
-#pragma unroll
-  for (int i = 0; i < kChunk / 4; ++i) s += v[i];
-  part[wave][lane] = s;
-  __syncthreads();
-  for (int w = 0; w < wave; ++w) base += part[w][lane];
-#pragma unroll
-  for (int i = 0; i < kChunk / 4; ++i) {
-    if (t0 + i < tiles) offsets[(int64_t)(t0 + i) * NB + dg] = base;
-    base += v[i];
-  }
-}
-
-// One pass: stable scatter of tile blockIdx.x by the digit at `shift`.  The
-// rank of a key is (its digit's count in earlier waves) + (in earlier items
-// of its wave) + (in lower lanes of its item), the last from DB ballots.
-template <int DB>
-__global__ __launch_bounds__(RT) void scatter_kernel(const uint32_t* __restrict__ kin, const int32_t* __restrict__ vin,
-                                                     uint32_t* __restrict__ kout, int32_t* __restrict__ vout, int n,
-                                                     int shift, const uint32_t* __restrict__ offsets, int tiles) {
-  constexpr int NB = 1 << DB, DPT = NB / RT;  // digits per thread (contiguous)
-  __shared__ uint32_t wcnt[4][NB];           // per-wave counts, then per-wave offsets
-  __shared__ uint32_t lstart[NB];            // tile-local start of each digit
-  __shared__ uint32_t gbase[NB];             // global position of a digit's span minus its tile-local start
-  __shared__ uint32_t lkeys[TILE];
-  __shared__ int32_t lvals[TILE];
-  __shared__ uint32_t s_wave[4];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int tile = blockIdx.x;
-  for (int i = tid; i < 4 * NB; i += RT) (&wcnt[0][0])[i] = 0u;
-  __syncthreads();
-  const int64_t t0 = (int64_t)tile * TILE;
-  const int cnt = (int)(n - t0 < TILE ? n - t0 : TILE);
-  const uint64_t below = (lane == 0) ? 0ull : (~0ull >> (64 - lane));
-  uint32_t key[ITEMS];
-  int32_t val[ITEMS];
-  uint32_t rank[ITEMS];
-#pragma unroll
-  for (int i = 0; i < ITEMS; ++i) {
-    const int q = tile_pos(wave, i, lane);
-    key[i] = q < cnt ? kin[t0 + q] : 0u;
-    val[i] = q < cnt ? vin[t0 + q] : 0;
-  }
-#pragma unroll
-  for (int i = 0; i < ITEMS; ++i) {
-    const bool valid = tile_pos(wave, i, lane) < cnt;
-    const uint32_t dg = (key[i] >> shift) & (uint32_t)(NB - 1);
-    uint64_t peers = __ballot(valid);
-#pragma unroll
-    for (int b = 0; b < DB; ++b) {
-      const bool bit = (dg >> b) & 1u;
-      const uint64_t m = __ballot(bit);
-      peers &= bit ? m : ~m;
-    }
-    // every lane reads the count before its group's lowest lane adds to it
-    const uint32_t before = valid ? wcnt[wave][dg] : 0u;
-    rank[i] = before + (uint32_t)__popcll(peers & below);
-    if (valid && (peers & below) == 0ull) wcnt[wave][dg] = before + (uint32_t)__popcll(peers);
-  }
-  __syncthreads();
-  uint32_t tc[DPT];
-  uint32_t tsum = 0;
-#pragma unroll
-  for (int j = 0; j < DPT; ++j) {
-    const int dg = tid * DPT + j;
-    uint32_t run = 0;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const uint32_t c = wcnt[w][dg];
-      wcnt[w][dg] = run;
-      run += c;
-    }
-    tc[j] = run;
-    tsum += run;
-  }
-  uint32_t total;
-  uint32_t lrun = block_exclusive_scan(tsum, s_wave, &total);
-#pragma unroll
-  for (int j = 0; j < DPT; ++j) {
-    const int dg = tid * DPT + j;
-    lstart[dg] = lrun;
-    gbase[dg] = offsets[(int64_t)tile * NB + dg] - lrun;
-    lrun += tc[j];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < ITEMS; ++i) {
-    if (tile_pos(wave, i, lane) < cnt) {
-      const uint32_t dg = (key[i] >> shift) & (uint32_t)(NB - 1);
-      const uint32_t lp = lstart[dg] + wcnt[wave][dg] + rank[i];
-      lkeys[lp] = key[i];
-      lvals[lp] = val[i];
-    }
-  }
-  __syncthreads();
-#pragma unroll 4
-  for (int j = tid; j < cnt; j += RT) {
-    const uint32_t k = lkeys[j];
-    const uint32_t pos = gbase[(k >> shift) & (uint32_t)(NB - 1)] + (uint32_t)j;
-    kout[pos] = k;
-    vout[pos] = lvals[j];
   }
 }
 
@@ -846,12 +601,6 @@ __global__ __launch_bounds__(256) void hot_final_kernel(float* const* __restrict
   }
 }
 
-int bits_for(int64_t x) {  // bits needed to hold 0..x
-  int b = 0;
-  while (b < 63 && (x >> b) != 0) ++b;
-  return b;
-}
-
 struct SparseLayout {
   size_t keys[2], vals[2], counts, sums, offsets, seg, seg_key, counters, hot, hseg, hoff, hcnt, hblocks, hpart, bytes;
   int64_t tiles;
@@ -981,19 +730,6 @@ int sparse_bufs(int64_t nnz, int d, void* ws, size_t ws_bytes, SparseLayout* L, 
   return DLRM_OK;
 }
 
-// The sort runs over the row bits only: positions are table-major (the
-// bags of table k come before those of table k + 1), so a stable sort by
-// row leaves equal rows in table order and every (table, row) key in one
-// run.  Digits of 8 bits, or 9 where that saves a pass (26 row bits: three
-// passes of 9 instead of four of 8).  The sorted keys and bag ids end in
-// buffer passes % 2.
-struct SortPlan {
-  int passes, digit_bits;
-};
-SortPlan sort_plan(int row_bits) {
-  const int p8 = (row_bits + 7) / 8, p9 = (row_bits + 8) / 9;
-  return p9 < p8 ? SortPlan{p9, 9} : SortPlan{p8, 8};
-}
 }  // namespace
 }  // namespace dlrm
 
@@ -1020,21 +756,12 @@ extern "C" int dlrm_embbag_bwd_sgd_prepare(int32_t K, const int64_t* rows, const
     hipLaunchKernelGGL(build_keys_kernel, dim3((unsigned)kblocks), dim3(256), 0, stream, indices, offsets, KB, B, kg,
                        row_bits, b.keys[0], b.vals[0]);
   }
+  // the sort runs over the row bits only: positions are table-major (the
+  // bags of table k come before those of table k + 1), so a stable sort by
+  // row leaves equal rows in table order and every (table, row) key in one run
   const SortPlan plan = sort_plan(row_bits);
   const unsigned tiles = (unsigned)L.tiles;
-  const dim3 chunk_grid((unsigned)ceil_div(L.tiles, kChunk), (unsigned)((1 << plan.digit_bits) / 64));
-  int cur = 0;
-  for (int pass = 0; pass < plan.passes; ++pass) {
-    const int shift = pass * plan.digit_bits;
-#define DLRM_PASS(DB)                                                                                                hipLaunchKernelGGL(tile_hist_kernel<DB>, dim3(tiles), dim3(RT), 0, stream, b.keys[cur], n, shift, b.counts,                          (int)tiles);                                                                                    hipLaunchKernelGGL(chunk_sum_kernel<DB>, chunk_grid, dim3(RT), 0, stream, b.counts, (int)tiles, b.sums);           hipLaunchKernelGGL(tile_offset_kernel<DB>, chunk_grid, dim3(RT), 0, stream, b.counts, b.sums, (int)tiles,                             b.offsets);                                                                                     hipLaunchKernelGGL(scatter_kernel<DB>, dim3(tiles), dim3(RT), 0, stream, b.keys[cur], b.vals[cur],                                   b.keys[cur ^ 1], b.vals[cur ^ 1], n, shift, b.offsets, (int)tiles)
-    if (plan.digit_bits == 9) {
-      DLRM_PASS(9);
-    } else {
-      DLRM_PASS(8);
-    }
-#undef DLRM_PASS
-    cur ^= 1;
-  }
+  const int cur = launch_sort(plan, b.keys, b.vals, b.counts, b.sums, b.offsets, n, stream);
   hipLaunchKernelGGL(heads_count_kernel, dim3(tiles), dim3(RT), 0, stream, b.keys[cur], n, b.counts);
   hipLaunchKernelGGL(heads_scan_kernel, dim3(1), dim3(RT), 0, stream, b.counts, (int)tiles, n, b.seg, b.counters);
   hipLaunchKernelGGL(heads_write_kernel, dim3(tiles), dim3(RT), 0, stream, b.keys[cur], n, b.counts, b.seg,
