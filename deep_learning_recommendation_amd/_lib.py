@@ -21,6 +21,7 @@ _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
+_F32 = ctypes.c_float
 
 _SIGNATURES = {
     "dlrm_abi_version": (ctypes.c_int, []),
@@ -50,6 +51,23 @@ _SIGNATURES = {
     "dlrm_embbag_bwd_sgd_noalloc": (ctypes.c_int, [_P, _I32, _I32, _P, _P, _P, _I64, _I64, _P, _I64, _I64,
                                                    ctypes.c_float, _P]),
     "dlrm_check_indices": (ctypes.c_int, [_P, _P, _I32, _I64, _P, _P, _P]),
+    "dlrm_token_embed_fwd": (ctypes.c_int, [_P, _I32, _I64, _I32, _P, _I64, _F32, _P, _I32, _I64, _P]),
+    "dlrm_token_embed_bwd_workspace_size": (_SZ, [_I64, _I64, _I32]),
+    "dlrm_token_embed_bwd": (ctypes.c_int, [_P, _I64, _P, _I32, _I64, _I64, _I32, _F32, _P, _I32, _P, _SZ, _P]),
+    "dlrm_dropout": (ctypes.c_int, [_P, _I64, _P, _I64, _I32, _I64, _I64, _F32, _P, _P]),
+    "dlrm_add_rmsnorm_fwd": (ctypes.c_int, [_P, _I64, _P, _I64, _I32, _P, _I64, _I32, _F32, _F32, _P, _P, _I64, _P,
+                                            _I32, _I64, _P, _P, _P]),
+    "dlrm_add_rmsnorm_bwd_workspace_size": (_SZ, [_I64, _I32]),
+    "dlrm_add_rmsnorm_bwd": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _I64, _I32, _P, _P, _I64, _I32, _F32, _P, _P, _I64,
+                                            _P, _I64, _P, _P, _SZ, _P]),
+    "dlrm_linattn_workspace_size": (_SZ, [_I64, _I32, _I64, _I32, _I32]),
+    "dlrm_linattn_fwd": (ctypes.c_int, [_P, _I64, _I64] * 3 + [_I32, _P, _I64, _I32, _I64, _I32, _I32, _P, _F32, _P, _P,
+                                                              _I64, _I64, _P, _P, _SZ, _P]),
+    "dlrm_linattn_bwd_workspace_size": (_SZ, [_I64, _I32, _I64, _I32, _I32]),
+    "dlrm_linattn_bwd": (ctypes.c_int, [_P, _I64, _I64] * 4 + [_I32, _P, _I64, _I32, _I64, _I32, _I32, _P, _F32, _P, _P] +
+                         [_P, _I64, _I64] * 3 + [_P, _P, _SZ, _P]),
+    "dlrm_linattn_step": (ctypes.c_int, [_P, _I64, _I64] * 3 + [_I32, _I64, _I32, _I32, _I32, _P, _F32, _P, _P, _P, _I64,
+                                                               _I64, _P]),
 }
 
 EXPORTS = tuple(_SIGNATURES)
@@ -122,6 +140,12 @@ def _dtype_code(t) -> int:
     import torch
 
     return DLRM_BF16 if t.dtype == torch.bfloat16 else DLRM_F32
+
+
+def _row_dtype_code(t) -> int:
+    import torch
+
+    return DLRM_I8 if t.dtype == torch.int8 else _dtype_code(t)
 
 
 def dlrm_abi_version() -> int:
@@ -254,3 +278,110 @@ def dlrm_embbag_bwd_sgd_apply(table_ptrs, K: int, d: int, rows, B: int, nnz: int
 def dlrm_check_indices(indices, offsets, K: int, B: int, rows_dev, bad_count, stream=None) -> None:
     _check("dlrm_check_indices", lib().dlrm_check_indices(_ptr(indices), _ptr(offsets), K, B, _ptr(rows_dev),
                                                            _ptr(bad_count), _stream(stream)))
+
+
+# The behaviour-history calls (one new event at a time, short histories) are
+# small enough for the call itself to matter: pointers and streams go as plain
+# integers, which the argument types above convert.
+
+def _addr(t) -> int | None:
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream) -> int:
+    import torch
+
+    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+
+
+def _bytes(ws) -> int:
+    return 0 if ws is None else ws.numel() * ws.element_size()
+
+
+def _heads(t):
+    """Address, row stride and head stride of a [rows][heads][width] tensor
+    whose last dimension is contiguous."""
+    if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] > 1):
+        raise ValueError("expected [rows][heads][width] with a contiguous last dimension")
+    return t.data_ptr(), t.stride(0), t.stride(1)
+
+
+def dlrm_token_embed_fwd(table, rows: int, d: int, tokens, n: int, scale: float, out, out_ld: int,
+                         stream=None) -> None:
+    """out[i] = scale * table[tokens[i]]; a token outside [0, rows) gives zeros."""
+    _check("dlrm_token_embed_fwd", lib().dlrm_token_embed_fwd(
+        _addr(table), _dtype_code(table), rows, d, _addr(tokens), n, scale, _addr(out), _dtype_code(out), out_ld,
+        _raw_stream(stream)))
+
+
+def dlrm_token_embed_bwd_workspace_size(n: int, rows: int, d: int) -> int:
+    return int(lib().dlrm_token_embed_bwd_workspace_size(n, rows, d))
+
+
+def dlrm_token_embed_bwd(tokens, n: int, dout, dout_ld: int, rows: int, d: int, scale: float, dtable,
+                         accumulate: bool, ws, stream=None) -> None:
+    """The fp32 table gradient, summed by sorted tokens (added to dtable with
+    ``accumulate``, else every row written)."""
+    _check("dlrm_token_embed_bwd", lib().dlrm_token_embed_bwd(
+        _addr(tokens), n, _addr(dout), _dtype_code(dout), dout_ld, rows, d, scale, _addr(dtable), int(accumulate),
+        _addr(ws), _bytes(ws), _raw_stream(stream)))
+
+
+def dlrm_dropout(x, x_ld: int, y, y_ld: int, rows: int, cols: int, p: float, rng, stream=None) -> None:
+    """y = x * mask / (1 - p); rng: device int64 [2] = (seed, offset).  The
+    backward pass is the same call on the gradient."""
+    _check("dlrm_dropout", lib().dlrm_dropout(_addr(x), x_ld, _addr(y), y_ld, _dtype_code(x), rows, cols, p,
+                                              _addr(rng), _raw_stream(stream)))
+
+
+def dlrm_add_rmsnorm_fwd(x, x_ld: int, res, res_ld: int, w, n: int, d: int, eps: float, p: float, rng, h, h_ld: int,
+                         y, y_ld: int, scale_bias, rstd, stream=None) -> None:
+    """h = res + dropout(x), y = h / rms(h) * w; an int8 y comes with
+    ``scale_bias`` = fp32 [n][2] (value = scale * q + bias, bias 0)."""
+    _check("dlrm_add_rmsnorm_fwd", lib().dlrm_add_rmsnorm_fwd(
+        _addr(x), x_ld, _addr(res), res_ld, _dtype_code(x), _addr(w), n, d, eps, p, _addr(rng), _addr(h), h_ld,
+        _addr(y), _row_dtype_code(y), y_ld, _addr(scale_bias), _addr(rstd), _raw_stream(stream)))
+
+
+def dlrm_add_rmsnorm_bwd_workspace_size(n: int, d: int) -> int:
+    return int(lib().dlrm_add_rmsnorm_bwd_workspace_size(n, d))
+
+
+def dlrm_add_rmsnorm_bwd(dy, dy_ld: int, dh, dh_ld: int, h, h_ld: int, w, rstd, n: int, d: int, p: float, rng, dx,
+                         dx_ld: int, dres, dres_ld: int, dw, ws, stream=None) -> None:
+    _check("dlrm_add_rmsnorm_bwd", lib().dlrm_add_rmsnorm_bwd(
+        _addr(dy), dy_ld, _addr(dh), dh_ld, _addr(h), h_ld, _dtype_code(dy), _addr(w), _addr(rstd), n, d, p,
+        _addr(rng), _addr(dx), dx_ld, _addr(dres), dres_ld, _addr(dw), _addr(ws), _bytes(ws), _raw_stream(stream)))
+
+
+def dlrm_linattn_workspace_size(B: int, H: int, max_len: int, dk: int, dv: int) -> int:
+    return int(lib().dlrm_linattn_workspace_size(B, H, max_len, dk, dv))
+
+
+def dlrm_linattn_fwd(q, k, v, offsets, B: int, H: int, max_len: int, dk: int, dv: int, decay, scale: float, state0, o,
+                     state, ws, stream=None) -> None:
+    """Linear attention over the B histories of ``offsets``; q, k, v, o are
+    [rows][heads][width] tensors (views of one projection's output will do)."""
+    _check("dlrm_linattn_fwd", lib().dlrm_linattn_fwd(
+        *_heads(q), *_heads(k), *_heads(v), _dtype_code(q), _addr(offsets), B, H, max_len, dk, dv, _addr(decay), scale,
+        _addr(state0), *_heads(o), _addr(state), _addr(ws), _bytes(ws), _raw_stream(stream)))
+
+
+def dlrm_linattn_bwd_workspace_size(B: int, H: int, max_len: int, dk: int, dv: int) -> int:
+    return int(lib().dlrm_linattn_bwd_workspace_size(B, H, max_len, dk, dv))
+
+
+def dlrm_linattn_bwd(q, k, v, do, offsets, B: int, H: int, max_len: int, dk: int, dv: int, decay, scale: float, state0,
+                     dstate, dq, dk_out, dv_out, dstate0, ws, stream=None) -> None:
+    _check("dlrm_linattn_bwd", lib().dlrm_linattn_bwd(
+        *_heads(q), *_heads(k), *_heads(v), *_heads(do), _dtype_code(q), _addr(offsets), B, H, max_len, dk, dv,
+        _addr(decay), scale, _addr(state0), _addr(dstate), *_heads(dq), *_heads(dk_out), *_heads(dv_out),
+        _addr(dstate0), _addr(ws), _bytes(ws), _raw_stream(stream)))
+
+
+def dlrm_linattn_step(q, k, v, B: int, H: int, dk: int, dv: int, decay, scale: float, state, slots, o,
+                      stream=None) -> None:
+    """One new event per user on a pool of states, updated in place."""
+    _check("dlrm_linattn_step", lib().dlrm_linattn_step(
+        *_heads(q), *_heads(k), *_heads(v), _dtype_code(q), B, H, dk, dv, _addr(decay), scale, _addr(state),
+        _addr(slots), *_heads(o), _raw_stream(stream)))

@@ -24,7 +24,8 @@ FLAGS = [
     f"-I{INCLUDE}",
 ]
 
-LIBDLRM_SOURCES = ["abi.hip", "embbag.hip", "interact.hip", "gemm.hip", "mlp.hip", "sparse.hip"]
+LIBDLRM_SOURCES = ["abi.hip", "embbag.hip", "interact.hip", "gemm.hip", "mlp.hip", "sparse.hip", "token.hip",
+                   "dropout.hip", "norm.hip", "linattn.hip"]
 
 
 def _compile(src: str, obj: str) -> None:

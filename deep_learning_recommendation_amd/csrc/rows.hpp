@@ -1,0 +1,87 @@
+// Row pieces: VE consecutive elements of an activation row (fp32, or bf16
+// bits) as one load or store, in fp32 registers.
+#pragma once
+
+#include "common.hpp"
+
+namespace dlrm {
+
+inline size_t elem_size(int32_t dtype) { return dtype == DLRM_F32 ? 4 : 2; }
+inline bool is_activation(int32_t dtype) { return dtype == DLRM_F32 || dtype == DLRM_BF16; }
+// whether p and a row pitch of ld elements keep every row aligned to `bytes`
+inline bool rows_aligned(const void* p, int64_t ld, size_t elem, size_t bytes) {
+  return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0 && (((size_t)ld * elem) & (bytes - 1)) == 0;
+}
+
+// VE elements of T as they lie in memory: 16 bytes, or 8 for four bf16.
+template <class T, int VE>
+struct Piece;
+
+template <>
+struct Piece<float, 4> {
+  float4 u;
+  __device__ __forceinline__ void load(const float* p) { u = *reinterpret_cast<const float4*>(p); }
+  __device__ __forceinline__ void get(float (&v)[4]) const { v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w; }
+  __device__ __forceinline__ void set(const float (&v)[4]) { u = make_float4(v[0], v[1], v[2], v[3]); }
+  __device__ __forceinline__ void store(float* p) const { *reinterpret_cast<float4*>(p) = u; }
+};
+template <>
+struct Piece<uint16_t, 4> {
+  uint2 u;
+  __device__ __forceinline__ void load(const uint16_t* p) { u = *reinterpret_cast<const uint2*>(p); }
+  __device__ __forceinline__ void get(float (&v)[4]) const {
+    v[0] = __uint_as_float(u.x << 16); v[1] = __uint_as_float(u.x & 0xffff0000u);
+    v[2] = __uint_as_float(u.y << 16); v[3] = __uint_as_float(u.y & 0xffff0000u);
+  }
+  __device__ __forceinline__ void set(const float (&v)[4]) {
+    u = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+  }
+  __device__ __forceinline__ void store(uint16_t* p) const { *reinterpret_cast<uint2*>(p) = u; }
+};
+template <>
+struct Piece<float, 8> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+  __device__ __forceinline__ void set(const float (&v)[8]) {
+    a = make_float4(v[0], v[1], v[2], v[3]);
+    b = make_float4(v[4], v[5], v[6], v[7]);
+  }
+  __device__ __forceinline__ void store(float* p) const {
+    reinterpret_cast<float4*>(p)[0] = a;
+    reinterpret_cast<float4*>(p)[1] = b;
+  }
+};
+template <>
+struct Piece<uint16_t, 8> {
+  uint4 u;
+  __device__ __forceinline__ void load(const uint16_t* p) { u = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    v[0] = __uint_as_float(u.x << 16); v[1] = __uint_as_float(u.x & 0xffff0000u);
+    v[2] = __uint_as_float(u.y << 16); v[3] = __uint_as_float(u.y & 0xffff0000u);
+    v[4] = __uint_as_float(u.z << 16); v[5] = __uint_as_float(u.z & 0xffff0000u);
+    v[6] = __uint_as_float(u.w << 16); v[7] = __uint_as_float(u.w & 0xffff0000u);
+  }
+  __device__ __forceinline__ void set(const float (&v)[8]) {
+    u = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                   pack_bf16x2(v[6], v[7]));
+  }
+  __device__ __forceinline__ void store(uint16_t* p) const { *reinterpret_cast<uint4*>(p) = u; }
+};
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(uint16_t x) { return bf16_to_f32(x); }
+template <class T>
+__device__ __forceinline__ T from_f32(float x);
+template <>
+__device__ __forceinline__ float from_f32<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ uint16_t from_f32<uint16_t>(float x) { return f32_to_bf16(x); }
+
+}  // namespace dlrm

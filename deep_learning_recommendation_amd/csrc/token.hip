@@ -1,0 +1,342 @@
+// Token embedding: lookup with a scale, and the gradient of its table by
+// sorted tokens.
+//
+//   out[i] = scale * T[t_i]                    (+0 for a token outside the table)
+//   dT[r]  = scale * sum over i with t_i = r of dout[i]
+//
+// Lookup.  Bound by memory: n rows read (a popular row from cache), n rows
+// written, eight bytes of token each.  A group of lanes covers one row with
+// 16-byte pieces, and each group keeps kRows rows in flight.
+//
+// Gradient.  The positions are sorted by token (radix_sort.hpp: stable, so a
+// row's positions stay in order), which turns the scattered sums into runs.
+// The sorted list is cut into chunks of kChunkLen positions whatever the runs
+// are, one lane group per chunk: the load is even for uniform tokens and for
+// a popular token with 1e5 occurrences alike, without a list of runs.  A run
+// inside a chunk goes straight to its table row; a run that crosses chunk
+// ends leaves one partial sum per chunk (head: it began earlier; tail: it
+// begins here and goes on), and a second kernel adds a run's partials in a
+// fixed order.  Every row is written once, by one group: no atomics.
+#include "common.hpp"
+#include "radix_sort.hpp"
+#include "rows.hpp"
+
+namespace dlrm {
+namespace {
+
+// lanes per row: enough for d / VE pieces, a power of two up to a wave
+int group_log2(int pieces) {
+  int g = 0;
+  while ((1 << g) < pieces && g < 6) ++g;
+  return g;
+}
+
+// ------------------------------------------------------------------ lookup
+
+constexpr int kRows = 4;
+
+template <class TI, class TO, int VE>
+__global__ __launch_bounds__(256) void token_fwd_kernel(const TI* __restrict__ table, int64_t rows, int d,
+                                                        const int64_t* __restrict__ tokens, int64_t n, float scale,
+                                                        TO* __restrict__ out, int64_t out_ld, int g_log2) {
+  const int GL = 1 << g_log2, gl = threadIdx.x & (GL - 1);
+  const int64_t groups = 256 >> g_log2;
+  const int64_t i0 = ((int64_t)blockIdx.x * groups + (threadIdx.x >> g_log2)) * kRows;
+  if (i0 >= n) return;
+  int64_t t[kRows];
+#pragma unroll
+  for (int j = 0; j < kRows; ++j) t[j] = i0 + j < n ? tokens[i0 + j] : -1;
+  for (int col = gl * VE; col < d; col += GL * VE) {
+    Piece<TI, VE> in[kRows];
+#pragma unroll
+    for (int j = 0; j < kRows; ++j)
+      if (t[j] >= 0 && t[j] < rows) in[j].load(table + t[j] * d + col);
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      if (i0 + j >= n) continue;
+      float v[VE];
+      if (t[j] >= 0 && t[j] < rows) {
+        in[j].get(v);
+#pragma unroll
+        for (int c = 0; c < VE; ++c) v[c] *= scale;
+      } else {
+#pragma unroll
+        for (int c = 0; c < VE; ++c) v[c] = 0.f;
+      }
+      Piece<TO, VE> o;
+      o.set(v);
+      o.store(out + (i0 + j) * out_ld + col);
+    }
+  }
+}
+
+template <class TI, class TO, int VE>
+int launch_fwd(const void* table, int64_t rows, int d, const int64_t* tokens, int64_t n, float scale, void* out,
+               int64_t out_ld, hipStream_t stream) {
+  const int g = group_log2(d / VE);
+  const int64_t blocks = ceil_div(n, (int64_t)(256 >> g) * kRows);
+  if (blocks > 0x7fffffffLL) return DLRM_E_UNSUPPORTED;
+  hipLaunchKernelGGL((token_fwd_kernel<TI, TO, VE>), dim3((unsigned)blocks), dim3(256), 0, stream,
+                     static_cast<const TI*>(table), rows, d, tokens, n, scale, static_cast<TO*>(out), out_ld, g);
+  return launch_status();
+}
+
+// ------------------------------------------------------------------ gradient
+
+constexpr int kChunkLen = 64;  // sorted positions per chunk
+
+// Keys (the token, or `rows` for one that names no row: those sort last) and
+// positions; and, unless the gradient is added to what the table gradient
+// holds, +0 into every row of it.
+__global__ __launch_bounds__(256) void token_keys_kernel(const int64_t* __restrict__ tokens, int n, int64_t rows,
+                                                         uint32_t* __restrict__ keys, int32_t* __restrict__ vals,
+                                                         float4* __restrict__ zero, int64_t zero4) {
+  const int64_t at = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, step = (int64_t)gridDim.x * blockDim.x;
+  for (int64_t i = at; i < n; i += step) {
+    const int64_t t = tokens[i];
+    keys[i] = (uint32_t)(t >= 0 && t < rows ? t : rows);
+    vals[i] = (int32_t)i;
+  }
+  for (int64_t i = at; i < zero4; i += step) zero[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+}
+
+template <int VE>
+__device__ __forceinline__ void put_row(float* p, const float (&acc)[VE], float scale, bool add) {
+#pragma unroll
+  for (int c = 0; c < VE; c += 4) {
+    float4 o = make_float4(scale * acc[c], scale * acc[c + 1], scale * acc[c + 2], scale * acc[c + 3]);
+    if (add) {
+      const float4 b = *reinterpret_cast<const float4*>(p + c);
+      o.x += b.x; o.y += b.y; o.z += b.z; o.w += b.w;
+    }
+    *reinterpret_cast<float4*>(p + c) = o;
+  }
+}
+
+template <int VE>
+__device__ __forceinline__ void put_part(float* p, const float (&acc)[VE]) {
+#pragma unroll
+  for (int c = 0; c < VE; c += 4)
+    *reinterpret_cast<float4*>(p + c) = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
+}
+
+// One lane group per chunk and column slice (blockIdx.y).
+template <class T, int VE, int U>
+__global__ __launch_bounds__(256) void token_chunk_kernel(const uint32_t* __restrict__ keys,
+                                                          const int32_t* __restrict__ vals, int n, uint32_t rows,
+                                                          const T* __restrict__ dout, int64_t ld, int d, int g_log2,
+                                                          float scale, bool add, float* __restrict__ dtable,
+                                                          float* __restrict__ head, float* __restrict__ tail) {
+  const int GL = 1 << g_log2, gl = threadIdx.x & (GL - 1);
+  const int64_t chunk = (int64_t)blockIdx.x * (256 >> g_log2) + (threadIdx.x >> g_log2);
+  const int64_t c0 = chunk * kChunkLen;
+  if (c0 >= n) return;  // whole group
+  const int len = (int)(n - c0 < kChunkLen ? n - c0 : kChunkLen);
+  const int col = ((int)blockIdx.y * GL + gl) * VE;
+  const bool on = col < d;
+  uint32_t cur = keys[c0];
+  if (cur >= rows) return;  // padding only
+  bool open = c0 > 0 && keys[c0 - 1] == cur;  // the run began before this chunk
+  float acc[VE];
+#pragma unroll
+  for (int c = 0; c < VE; ++c) acc[c] = 0.f;
+  auto close = [&]() {  // the run of `cur` ends here
+    if (!on) return;
+    if (open) put_part<VE>(head + chunk * d + col, acc);
+    else put_row<VE>(dtable + (int64_t)cur * d + col, acc, scale, add);
+  };
+  for (int q0 = 0; q0 < len; q0 += GL) {
+    const int m = min(GL, len - q0);
+    const uint32_t my_key = gl < m ? keys[c0 + q0 + gl] : rows;
+    const int32_t my_pos = gl < m ? vals[c0 + q0 + gl] : 0;
+    for (int u0 = 0; u0 < m; u0 += U) {
+      Piece<T, VE> in[U];
+      uint32_t key[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int src = u0 + u < m ? u0 + u : m - 1;
+        key[u] = (uint32_t)__shfl((int)my_key, src, GL);
+        const int64_t pos = __shfl(my_pos, src, GL);
+        if (u0 + u >= m) key[u] = rows;
+        if (on && key[u] < rows) in[u].load(dout + pos * ld + col);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (key[u] >= rows) continue;
+        if (key[u] != cur) {
+          close();
+          cur = key[u];
+          open = false;
+#pragma unroll
+          for (int c = 0; c < VE; ++c) acc[c] = 0.f;
+        }
+        if (on) {
+          float v[VE];
+          in[u].get(v);
+#pragma unroll
+          for (int c = 0; c < VE; ++c) acc[c] += v[c];
+        }
+      }
+    }
+  }
+  const bool goes_on = c0 + len < n && keys[c0 + len] == cur;
+  if (!goes_on) close();
+  else if (on) put_part<VE>((open ? head : tail) + chunk * d + col, acc);
+}
+
+// One wave per chunk whose last run begins in it and goes on: tail of this
+// chunk plus the heads of the chunks that the run reaches, the wave's lane
+// groups taking every groups-th partial, then added across groups.
+template <int VE>
+__global__ __launch_bounds__(256) void token_join_kernel(const uint32_t* __restrict__ keys, int n, uint32_t rows, int d,
+                                                         int g_log2, float scale, bool add,
+                                                         float* __restrict__ dtable, const float* __restrict__ head,
+                                                         const float* __restrict__ tail) {
+  const int lane = threadIdx.x & 63;
+  const int64_t chunk = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int64_t c0 = chunk * kChunkLen, c1 = c0 + kChunkLen;
+  if (c1 >= n) return;
+  const uint32_t key = keys[c1 - 1];
+  if (key >= rows || keys[c1] != key) return;
+  if (keys[c0] == key && c0 > 0 && keys[c0 - 1] == key) return;  // began earlier
+  int64_t m = 0;  // chunks after this one that the run reaches
+  for (;;) {
+    const int64_t p = (chunk + 1 + m + lane) * kChunkLen;
+    const uint64_t miss = __ballot(!(p < n && keys[p] == key));
+    if (miss) {
+      m += __ffsll((long long)miss) - 1;
+      break;
+    }
+    m += 64;
+  }
+  const int GL = 1 << g_log2, gl = lane & (GL - 1), groups = 64 >> g_log2;
+  const int col = ((int)blockIdx.y * GL + gl) * VE;
+  const bool on = col < d;
+  float acc[VE];
+#pragma unroll
+  for (int c = 0; c < VE; ++c) acc[c] = 0.f;
+  for (int64_t i = lane >> g_log2; i <= m; i += groups) {
+    const float* p = i == 0 ? tail + chunk * d : head + (chunk + i) * d;
+    if (on) {
+#pragma unroll
+      for (int c = 0; c < VE; ++c) acc[c] += p[col + c];
+    }
+  }
+  for (int o = GL; o < 64; o <<= 1) {
+#pragma unroll
+    for (int c = 0; c < VE; ++c) acc[c] += __shfl_xor(acc[c], o, 64);
+  }
+  if (on && lane < GL) put_row<VE>(dtable + (int64_t)key * d + col, acc, scale, add);
+}
+
+struct TokenLayout {
+  size_t keys[2], vals[2], counts, sums, offsets, head, tail, bytes;
+};
+
+void token_layout(int64_t n, int d, TokenLayout* L) {
+  Carver cv(nullptr);
+  auto take = [&](size_t bytes) {
+    cv.take<char>(bytes);
+    return cv.used - bytes;
+  };
+  const int64_t m = n > 0 ? n : 1, tiles = ceil_div(m, TILE), chunks = ceil_div(m, kChunkLen);
+  for (int i = 0; i < 2; ++i) L->keys[i] = take(4 * (size_t)m);
+  for (int i = 0; i < 2; ++i) L->vals[i] = take(4 * (size_t)m);
+  L->counts = take(4 * (size_t)kMaxDigits * tiles);
+  L->sums = take(4 * (size_t)kMaxDigits * ceil_div(tiles, kChunk));
+  L->offsets = take(4 * (size_t)kMaxDigits * tiles);
+  L->head = take(4 * (size_t)chunks * d);
+  L->tail = take(4 * (size_t)chunks * d);
+  L->bytes = cv.bytes();
+}
+
+template <class T, int VE>
+int launch_bwd(const uint32_t* keys, const int32_t* vals, int n, uint32_t rows, const void* dout, int64_t ld, int d,
+               float scale, bool add, float* dtable, float* head, float* tail, hipStream_t stream) {
+  const int64_t chunks = ceil_div(n, kChunkLen);
+  const int g = group_log2(d / VE);
+  const unsigned slices = (unsigned)ceil_div(d / VE, 1 << g);
+  hipLaunchKernelGGL((token_chunk_kernel<T, VE, 8>), dim3((unsigned)ceil_div(chunks, 256 >> g), slices), dim3(256), 0,
+                     stream, keys, vals, n, rows, static_cast<const T*>(dout), ld, d, g, scale, add, dtable, head,
+                     tail);
+  if (chunks > 1)
+    hipLaunchKernelGGL((token_join_kernel<VE>), dim3((unsigned)ceil_div(chunks, 4), slices), dim3(256), 0, stream, keys,
+                       n, rows, d, g, scale, add, dtable, head, tail);
+  return launch_status();
+}
+
+// what both directions ask of a row's width, pitch and alignment
+bool rows_ok(const void* p, int64_t ld, int32_t dtype, int32_t d) {
+  const size_t e = elem_size(dtype);
+  return p && ld >= d && rows_aligned(p, ld, e, 4 * e);
+}
+
+}  // namespace
+}  // namespace dlrm
+
+using namespace dlrm;
+
+extern "C" int dlrm_token_embed_fwd(const void* table, int32_t table_dtype, int64_t rows, int32_t d,
+                                    const int64_t* tokens, int64_t n, float scale, void* out, int32_t out_dtype,
+                                    int64_t out_ld, hipStream_t stream) {
+  if (!is_activation(table_dtype) || !is_activation(out_dtype) || rows < 1 || n < 0) return DLRM_E_INVALID;
+  if (d < 4 || d > 1024 || (d % 4) != 0) return DLRM_E_INVALID;
+  if (n == 0) return DLRM_OK;
+  if (!tokens || !rows_ok(table, d, table_dtype, d) || !rows_ok(out, out_ld, out_dtype, d)) return DLRM_E_INVALID;
+  if (table_dtype == DLRM_BF16 && out_dtype == DLRM_BF16) {
+    if (d % 8 == 0 && rows_aligned(table, d, 2, 16) && rows_aligned(out, out_ld, 2, 16))
+      return launch_fwd<uint16_t, uint16_t, 8>(table, rows, d, tokens, n, scale, out, out_ld, stream);
+    return launch_fwd<uint16_t, uint16_t, 4>(table, rows, d, tokens, n, scale, out, out_ld, stream);
+  }
+  if (table_dtype == DLRM_BF16)
+    return launch_fwd<uint16_t, float, 4>(table, rows, d, tokens, n, scale, out, out_ld, stream);
+  if (out_dtype == DLRM_BF16)
+    return launch_fwd<float, uint16_t, 4>(table, rows, d, tokens, n, scale, out, out_ld, stream);
+  return launch_fwd<float, float, 4>(table, rows, d, tokens, n, scale, out, out_ld, stream);
+}
+
+extern "C" size_t dlrm_token_embed_bwd_workspace_size(int64_t n, int64_t rows, int32_t d) {
+  (void)rows;
+  if (n < 0 || d < 0) return 0;
+  TokenLayout L;
+  token_layout(n, d, &L);
+  return L.bytes;
+}
+
+extern "C" int dlrm_token_embed_bwd(const int64_t* tokens, int64_t n, const void* dout, int32_t dout_dtype,
+                                    int64_t dout_ld, int64_t rows, int32_t d, float scale, float* dtable,
+                                    int32_t accumulate, void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (!is_activation(dout_dtype) || rows < 1 || n < 0 || n > 0x7fffffffLL) return DLRM_E_INVALID;
+  if (d < 4 || d > 1024 || (d % 4) != 0 || !dtable || !aligned16(dtable)) return DLRM_E_INVALID;
+  if (n > 0 && (!tokens || !rows_ok(dout, dout_ld, dout_dtype, d))) return DLRM_E_INVALID;
+  if (rows >= 0xffffffffLL) return DLRM_E_UNSUPPORTED;
+  TokenLayout L;
+  token_layout(n, d, &L);
+  if (!ws || ws_bytes < L.bytes) return DLRM_E_WORKSPACE;
+  if (reinterpret_cast<uintptr_t>(ws) & 255u) return DLRM_E_INVALID;
+  char* w = static_cast<char*>(ws);
+  uint32_t* const keys[2] = {reinterpret_cast<uint32_t*>(w + L.keys[0]), reinterpret_cast<uint32_t*>(w + L.keys[1])};
+  int32_t* const vals[2] = {reinterpret_cast<int32_t*>(w + L.vals[0]), reinterpret_cast<int32_t*>(w + L.vals[1])};
+  auto u32 = [&](size_t at) { return reinterpret_cast<uint32_t*>(w + at); };
+  const bool add = accumulate != 0;
+  const int64_t zero4 = add ? 0 : rows * d / 4;
+  const int64_t most = n > zero4 ? n : zero4;
+  if (most == 0) return DLRM_OK;
+  const int64_t blocks = ceil_div(most, 256);
+  hipLaunchKernelGGL(token_keys_kernel, dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256), 0, stream, tokens,
+                     (int)n, rows, keys[0], vals[0], reinterpret_cast<float4*>(dtable), zero4);
+  if (n == 0) return launch_status();
+  const int cur = launch_sort(sort_plan(bits_for(rows)), keys, vals, u32(L.counts), u32(L.sums), u32(L.offsets), (int)n,
+                              stream);
+  float* head = reinterpret_cast<float*>(w + L.head);
+  float* tail = reinterpret_cast<float*>(w + L.tail);
+  const uint32_t r = (uint32_t)rows;
+  if (dout_dtype == DLRM_F32)
+    return launch_bwd<float, 4>(keys[cur], vals[cur], (int)n, r, dout, dout_ld, d, scale, add, dtable, head, tail,
+                                stream);
+  if (d % 8 == 0 && rows_aligned(dout, dout_ld, 2, 16))
+    return launch_bwd<uint16_t, 8>(keys[cur], vals[cur], (int)n, r, dout, dout_ld, d, scale, add, dtable, head, tail,
+                                   stream);
+  return launch_bwd<uint16_t, 4>(keys[cur], vals[cur], (int)n, r, dout, dout_ld, d, scale, add, dtable, head, tail,
+                                 stream);
+}

@@ -392,6 +392,188 @@ int dlrm_embbag_bwd_sgd_noalloc(float* const* tables, int32_t K, int32_t d, cons
 int dlrm_check_indices(const int64_t* indices, const int64_t* offsets, int32_t K, int64_t B,
                        const int64_t* rows_dev, int64_t* bad_count, hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Behaviour histories.
+ * A user's history is a ragged list of item tokens; the calls below turn it
+ * into vectors (a row of X, or an int8 table row for later lookups) and
+ * train that path.  Elements are DLRM_F32 or DLRM_BF16, every sum, statistic
+ * and state is fp32, and a bf16 result is rounded once (nearest even) when
+ * it is stored.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Token embedding lookup with a scale (forward).
+ *     out[i][c] = scale * T[tokens[i]][c],   c < d
+ * A token outside [0, rows) names no row (padding): its output row is +0.
+ *   table    [rows][d] of table_dtype.
+ *   tokens   int64 [n].
+ *   out      out_dtype, row i at out + i*out_ld (out_ld >= d).
+ *   Types:   DLRM_F32 and DLRM_BF16 in any combination.
+ *   Limits:  d % 4 == 0, 4 <= d <= 1024, rows >= 1, n >= 0; table, out and
+ *            their rows aligned to four elements (16 bytes fp32, 8 bytes
+ *            bf16).  bf16 to bf16 with 16-byte aligned rows moves twice as
+ *            many bytes per load.
+ */
+int dlrm_token_embed_fwd(const void* table, int32_t table_dtype, int64_t rows, int32_t d, const int64_t* tokens,
+                         int64_t n, float scale, void* out, int32_t out_dtype, int64_t out_ld, hipStream_t stream);
+
+/*
+ * Gradient of the lookup with respect to its table, by sorted tokens.
+ *     dtable[r][c] = scale * sum over i with tokens[i] == r of dout[i][c]
+ * (accumulate != 0: added to dtable, whose other rows are not touched;
+ * accumulate == 0: every row is written, rows without a token with +0).
+ * The tokens are sorted (stable radix sort of their positions), so a row's
+ * terms are added in position order in blocks that the sort fixes: no
+ * floating-point atomics, bitwise deterministic.  Tokens outside [0, rows)
+ * give no gradient.
+ *   dout     dout_dtype (DLRM_F32 or DLRM_BF16), row i at dout + i*dout_ld.
+ *   dtable   fp32 [rows][d], 16-byte aligned.
+ *   ws       dlrm_token_embed_bwd_workspace_size() bytes, 256-byte aligned.
+ *   Limits:  as the forward call, n < 2^31, rows < 2^32 - 1
+ *            (DLRM_E_UNSUPPORTED above).
+ */
+size_t dlrm_token_embed_bwd_workspace_size(int64_t n, int64_t rows, int32_t d);
+int dlrm_token_embed_bwd(const int64_t* tokens, int64_t n, const void* dout, int32_t dout_dtype, int64_t dout_ld,
+                         int64_t rows, int32_t d, float scale, float* dtable, int32_t accumulate, void* ws,
+                         size_t ws_bytes, hipStream_t stream);
+
+/*
+ * Dropout from a counter-based generator; the mask is never stored.
+ *     y[r][c] = keep(e) ? x[r][c] * 65536 / (65536 - cut) : +0,
+ *     e = r*cols + c,  cut = floor(65536 p + 1/2)
+ * keep(e): with (seed, offset) = rng[0..1] taken as 64-bit words, the four
+ * 32-bit output words of Philox4x32-10 (Salmon, Moraes, Dror and Shaw,
+ * "Parallel random numbers: as easy as 1, 2, 3", 2011) for the key seed and
+ * the counter (offset + e/8 mod 2^64, 0) hold eight 16-bit fields, low half
+ * first; e is kept when field e % 8 is at least cut.  So p is applied in
+ * steps of 2^-16, the factor keeps the mean exactly, and the mask does not
+ * depend on strides or types.  The gradient is the same call on dy with the
+ * same rng.  A dropped element is +0 whatever x holds (NaN and infinities
+ * too).
+ *   rng      DEVICE int64 [2]: read by the kernel, so a captured graph draws
+ *            new masks when the program moves the offset on the device by at
+ *            least ceil(rows*cols / 8) between replays.
+ *   x, y     dtype, rows at x + r*x_ld, y + r*y_ld; y may be x (same ld).
+ *   p        0 <= p <= 1 (p = 1: all zero).
+ *   Limits:  rows >= 0, 1 <= cols, rows * cols < 2^40; x and y aligned to
+ *            their element.
+ */
+int dlrm_dropout(const void* x, int64_t x_ld, void* y, int64_t y_ld, int32_t dtype, int64_t rows, int64_t cols,
+                 float p, const int64_t* rng, hipStream_t stream);
+
+/*
+ * Residual addition and root-mean-square norm (forward), with the branch's
+ * dropout and an optional int8 output.
+ *     h = res + dropout(x)           (dropout as dlrm_dropout over [n][d])
+ *     r = 1 / sqrt(mean over c of h[c]^2 + eps),   y[c] = h[c] * r * w[c]
+ *   x        dtype [n] rows of d at x + i*x_ld;  res likewise, nullable (0).
+ *   w        fp32 [d].
+ *   p, rng   dropout on x; p == 0: none (rng may be NULL).
+ *   h        nullable, dtype: the new residual stream.  The norm takes the
+ *            fp32 sum, not its rounded copy.  h may be x or res (same ld).
+ *   y        y_dtype: dtype, or DLRM_I8 with scale_bias fp32 [n][2]: per
+ *            row s = max |y| / 127, q = y / s rounded to nearest even,
+ *            (s, 0) stored, so the rows and pairs are table rows that
+ *            dlrm_embbag_fwd_lp reads (a row of zeros: s = 0, q = 0; a row
+ *            with a NaN: s = NaN, q = 0).
+ *   rstd     nullable fp32 [n], r for the backward call.
+ *   Limits:  1 <= d <= 16384, n >= 0, every ld >= d.  Rows of 16-byte
+ *            aligned pitch and base (8-byte for int8) with d % 8 == 0 take
+ *            the vector path.
+ */
+int dlrm_add_rmsnorm_fwd(const void* x, int64_t x_ld, const void* res, int64_t res_ld, int32_t dtype, const float* w,
+                         int64_t n, int32_t d, float eps, float p, const int64_t* rng, void* h, int64_t h_ld, void* y,
+                         int32_t y_dtype, int64_t y_ld, float* scale_bias, float* rstd, hipStream_t stream);
+
+/*
+ * Backward of dlrm_add_rmsnorm_fwd (outputs in the activation type).
+ *     g = dy * w,  t = dh + r g - h r^3 mean over c of (g h)
+ *     dres = t,  dx = dropout(t)  (same p, rng),  dw[c] = sum over rows of dy h r
+ *   dy       dtype;  dh nullable: the gradient that reaches h by the
+ *            residual stream.
+ *   h, rstd  the forward call's outputs.
+ *   dx, dres nullable (not both); dres may be dh or dy, dx may be dy or dh.
+ *   dw       fp32 [d], overwritten: per-block sums, then one pass over them
+ *            in a fixed order.
+ *   ws       dlrm_add_rmsnorm_bwd_workspace_size() bytes, 256-byte aligned.
+ */
+size_t dlrm_add_rmsnorm_bwd_workspace_size(int64_t n, int32_t d);
+int dlrm_add_rmsnorm_bwd(const void* dy, int64_t dy_ld, const void* dh, int64_t dh_ld, const void* h, int64_t h_ld,
+                         int32_t dtype, const float* w, const float* rstd, int64_t n, int32_t d, float p,
+                         const int64_t* rng, void* dx, int64_t dx_ld, void* dres, int64_t dres_ld, float* dw,
+                         void* ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * Linear attention with one decay per head, over ragged histories.
+ *     S_t = decay_h S_(t-1) + k_t v_t^T   (dk x dv, S_(-1) = state0 or 0)
+ *     o_t = scale * q_t S_t
+ * History b owns rows offsets[b] .. offsets[b+1] of q, k, v and o (it may be
+ * empty: its state is then state0).  Computed chunk by chunk with matrix
+ * instructions: inside a chunk by the masked, decayed products q_t . k_i,
+ * across chunks through the fp32 state; long histories are cut into segments
+ * that run at once, their states joined by a scan.
+ *   q, k     dtype, row i, head h at q + i*q_ts + h*q_hs, dk contiguous
+ *            elements (likewise k; v with dv elements; o with o_ts, o_hs).
+ *   offsets  int64 [B + 1], non-decreasing, offsets[0] >= 0 (device).
+ *   max_len  host: no history is longer (a precondition).
+ *   decay    fp32 [H], 0 <= decay <= 1: a constant of the layer (it gets no
+ *            gradient).
+ *   state0   nullable fp32 [B][H][dk][dv].
+ *   state    nullable fp32 [B][H][dk][dv]: S after each history's last row;
+ *            may be state0.
+ *   Rounding: DLRM_BF16 rounds the masked products and, for the product
+ *            with q, a copy of the state to bf16 (the matrix instructions'
+ *            operands); the state itself is updated from exact splits of its
+ *            operands and stays fp32.  DLRM_F32 multiplies in fp32.
+ *   ws       dlrm_linattn_workspace_size() bytes, 256-byte aligned (may be
+ *            0: then ws may be NULL).
+ *   Limits:  dk, dv multiples of 8, 8 .. 128; every row and head stride a
+ *            multiple of 8 elements and every base 16-byte aligned; state0
+ *            and state 16-byte aligned; B, H >= 1, B * H * 32 < 2^31.
+ */
+size_t dlrm_linattn_workspace_size(int64_t B, int32_t H, int64_t max_len, int32_t dk, int32_t dv);
+int dlrm_linattn_fwd(const void* q, int64_t q_ts, int64_t q_hs, const void* k, int64_t k_ts, int64_t k_hs,
+                     const void* v, int64_t v_ts, int64_t v_hs, int32_t dtype, const int64_t* offsets, int64_t B,
+                     int32_t H, int64_t max_len, int32_t dk, int32_t dv, const float* decay, float scale,
+                     const float* state0, void* o, int64_t o_ts, int64_t o_hs, float* state, void* ws,
+                     size_t ws_bytes, hipStream_t stream);
+
+/*
+ * Gradients of dlrm_linattn_fwd.  With U_t the gradient of S_t,
+ *     U_t = scale q_t do_t^T + W_t,  W_(t-1) = decay_h U_t,  W_last = dstate or 0
+ *     dq_t = scale S_t do_t,  dk_t = U_t v_t,  dv_t = U_t^T k_t,  dstate0 = W_(-1)
+ * so dq is the same attention of (do, v, k), and dk and dv are those of
+ * (v, do, q) and (k, q, do) backwards in time: one kernel, three roles in one
+ * launch.
+ *   do_      dtype, the gradient of o; dq, dk_, dv_ the outputs (dtype),
+ *            each with its row and head strides.
+ *   dstate   nullable fp32 [B][H][dk][dv], the gradient of `state`.
+ *   dstate0  nullable fp32 [B][H][dk][dv], the gradient of `state0`; must not
+ *            be dstate.
+ */
+size_t dlrm_linattn_bwd_workspace_size(int64_t B, int32_t H, int64_t max_len, int32_t dk, int32_t dv);
+int dlrm_linattn_bwd(const void* q, int64_t q_ts, int64_t q_hs, const void* k, int64_t k_ts, int64_t k_hs,
+                     const void* v, int64_t v_ts, int64_t v_hs, const void* do_, int64_t do_ts, int64_t do_hs,
+                     int32_t dtype, const int64_t* offsets, int64_t B, int32_t H, int64_t max_len, int32_t dk,
+                     int32_t dv, const float* decay, float scale, const float* state0, const float* dstate, void* dq,
+                     int64_t dq_ts, int64_t dq_hs, void* dk_, int64_t dk_ts, int64_t dk_hs, void* dv_, int64_t dv_ts,
+                     int64_t dv_hs, float* dstate0, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * One new event per user: the recurrent form of the attention above, in fp32.
+ *     S <- decay_h S + k v^T,  o = scale * q S
+ *   q, k, v, o  dtype, user b, head h at q + b*q_bs + h*q_hs.
+ *   state    fp32 [pool][H][dk][dv], updated in place.
+ *   slots    nullable int64 [B], distinct: user b's entry of the pool (NULL:
+ *            b).  A negative slot marks no user: o is +0, no state changes.
+ *   Limits:  dk, dv multiples of 8, 8 .. 128; bases and strides as above;
+ *            the pool may hold more than 2^32 bytes.
+ */
+int dlrm_linattn_step(const void* q, int64_t q_bs, int64_t q_hs, const void* k, int64_t k_bs, int64_t k_hs,
+                      const void* v, int64_t v_bs, int64_t v_hs, int32_t dtype, int64_t B, int32_t H, int32_t dk,
+                      int32_t dv, const float* decay, float scale, float* state, const int64_t* slots, void* o,
+                      int64_t o_bs, int64_t o_hs, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
