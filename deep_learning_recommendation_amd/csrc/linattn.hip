@@ -32,41 +32,538 @@ struct Roles {
   Role r[3];
 };
 
-// One block per history, head and role: the recurrence as it stands.
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kC = 64;       // rows per chunk
+constexpr int kThreads = 256;
+
+// Matrix products of 16 x 16 tiles.  A product takes fragments a (16 rows of
+// M) and b (16 columns of N) and holds, in lane 16 g + n, column n and rows
+// 4 g .. 4 g + 3.  The summed index may run in any order that a and b share;
+// two orders are used:
+//   wide  a head's width: lane group g holds kWide / 4 consecutive elements of
+//         its row;
+//   time  a chunk's rows: of tile i, lane group g holds rows 16 i + 4 g + r,
+//         r < 4, which is how a product whose M is time leaves them.
+// So the masked products go from one product's result to the next one's
+// operand in registers.
 template <class T>
-__global__ __launch_bounds__(128) void linattn_kernel(Roles roles, const int64_t* __restrict__ offsets, int H,
-                                                      const float* __restrict__ decay) {
-  __shared__ float S[128 * 128];
-  __shared__ float qs[128], ks[128];
-  const Role r = roles.r[blockIdx.y];
-  const int64_t b = blockIdx.x / H;
-  const int h = blockIdx.x - (int)b * H, j = threadIdx.x;
-  const int64_t beg = offsets[b], len = offsets[b + 1] - beg;
-  const float lam = decay[h];
-  const int64_t sb = (b * H + h) * r.dk * r.dv;
-  auto at = [&](int i) { return r.flip ? j * r.dk + i : i * r.dv + j; };
-  if (j < r.dv)
-    for (int i = 0; i < r.dk; ++i) S[i * 128 + j] = r.first ? r.first[sb + at(i)] : 0.f;
-  for (int64_t s = 0; s < len; ++s) {
-    const int64_t t = beg + (r.back ? len - 1 - s : s);
-    __syncthreads();
-    if (j < r.dk) {
-      qs[j] = to_f32(static_cast<const T*>(r.q.p)[t * r.q.ts + h * r.q.hs + j]);
-      ks[j] = to_f32(static_cast<const T*>(r.k.p)[t * r.k.ts + h * r.k.hs + j]) * r.kscale;
-    }
-    __syncthreads();
-    if (j >= r.dv) continue;
-    const float v = to_f32(static_cast<const T*>(r.v.p)[t * r.v.ts + h * r.v.hs + j]);
-    float acc = 0.f;
-    for (int i = 0; i < r.dk; ++i) {
-      const float u = (r.back ? 1.f : lam) * S[i * 128 + j] + ks[i] * v;
-      acc += qs[i] * u;
-      S[i * 128 + j] = r.back ? lam * u : u;
-    }
-    static_cast<T*>(const_cast<void*>(r.o.p))[t * r.o.ts + h * r.o.hs + j] = from_f32<T>(acc * r.oscale);
+struct Mat;
+
+template <>
+struct Mat<uint16_t> {
+  static constexpr int kWide = 32;  // summed elements per fragment, along a width
+  static constexpr int kTiles = 2;  // time tiles per fragment
+  static constexpr int kPiece = 8;  // elements per 16 bytes
+  using Frag = bf16x8;
+  static __device__ __forceinline__ Frag zero() { return __builtin_bit_cast(Frag, s16x8{0, 0, 0, 0, 0, 0, 0, 0}); }
+  static __device__ __forceinline__ Frag wide(const uint16_t* row, int g) {
+    return *reinterpret_cast<const Frag*>(row + 8 * g);
   }
-  if (r.last && j < r.dv)
-    for (int i = 0; i < r.dk; ++i) r.last[sb + at(i)] = S[i * 128 + j];
+  // columns of time-major LDS rows by transposing reads: lane s of a group of
+  // 16 addresses row s / 4 and columns 4 (s % 4) .. + 3 of the 16, and
+  // receives column s of the four rows
+  template <int PITCH>
+  static __device__ __forceinline__ Frag time(const uint16_t* base, int f, int lane, int col) {
+    s16x4 v[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint16_t* p = base + (32 * f + 16 * i + 4 * (lane >> 4) + ((lane & 15) >> 2)) * PITCH + col;
+      v[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (__attribute__((address_space(3))) s16x4*)((__attribute__((address_space(3))) char*)p));
+    }
+    return __builtin_bit_cast(Frag, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
+  }
+  static __device__ __forceinline__ int time_col(int lane, int step) { return step * (lane & 3); }
+  static __device__ __forceinline__ Frag pack(const f32x4* t) {
+    const uint4 u = make_uint4(pack_bf16x2(t[0][0], t[0][1]), pack_bf16x2(t[0][2], t[0][3]),
+                               pack_bf16x2(t[1][0], t[1][1]), pack_bf16x2(t[1][2], t[1][3]));
+    return __builtin_bit_cast(Frag, u);
+  }
+  static __device__ __forceinline__ f32x4 mma(Frag a, Frag b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+  }
+  // N products with a's elements times w: w a is split into three bf16 parts
+  // that hold all 24 bits, so the sums are those of fp32 factors
+  template <int N>
+  static __device__ __forceinline__ void mma_scaled(Frag a, const f32x4* w, const Frag* b, f32x4* c) {
+    f32x4 x[2];
+    const uint4 u = __builtin_bit_cast(uint4, a);
+    const uint32_t q[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i / 2][2 * (i % 2)] = __uint_as_float(q[i] << 16) * w[i / 2][2 * (i % 2)];
+      x[i / 2][2 * (i % 2) + 1] = __uint_as_float(q[i] & 0xffff0000u) * w[i / 2][2 * (i % 2) + 1];
+    }
+#pragma unroll
+    for (int part = 0; part < 3; ++part) {
+      const Frag p = pack(x);
+#pragma unroll
+      for (int n = 0; n < N; ++n) c[n] = mma(p, b[n], c[n]);
+      const uint4 v = __builtin_bit_cast(uint4, p);
+      const uint32_t h[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[i / 2][2 * (i % 2)] -= __uint_as_float(h[i] << 16);
+        x[i / 2][2 * (i % 2) + 1] -= __uint_as_float(h[i] & 0xffff0000u);
+      }
+    }
+  }
+  static __device__ __forceinline__ void put4(uint16_t* p, f32x4 v) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+  }
+  // bit e: element e of 16 bytes is not finite
+  static __device__ __forceinline__ uint32_t bad(uint4 u) {
+    const uint32_t q[4] = {u.x, u.y, u.z, u.w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      m |= (uint32_t)((q[i] & 0x7f80u) == 0x7f80u) << (2 * i);
+      m |= (uint32_t)((q[i] & 0x7f800000u) == 0x7f800000u) << (2 * i + 1);
+    }
+    return m;
+  }
+};
+
+template <>
+struct Mat<float> {
+  static constexpr int kWide = 16, kTiles = 1, kPiece = 4;
+  using Frag = f32x4;
+  static __device__ __forceinline__ Frag zero() { return f32x4{0.f, 0.f, 0.f, 0.f}; }
+  static __device__ __forceinline__ Frag wide(const float* row, int g) {
+    return *reinterpret_cast<const Frag*>(row + 4 * g);
+  }
+  template <int PITCH>
+  static __device__ __forceinline__ Frag time(const float* base, int f, int lane, int col) {
+    Frag v;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[r] = base[(16 * f + 4 * (lane >> 4) + r) * PITCH + col];
+    return v;
+  }
+  static __device__ __forceinline__ int time_col(int lane, int step) {
+    return step * ((lane & 15) >> 2) + (lane & 3);
+  }
+  static __device__ __forceinline__ Frag pack(const f32x4* t) { return t[0]; }
+  static __device__ __forceinline__ f32x4 mma(Frag a, Frag b, f32x4 c) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[r], b[r], c, 0, 0, 0);
+    return c;
+  }
+  template <int N>
+  static __device__ __forceinline__ void mma_scaled(Frag a, const f32x4* w, const Frag* b, f32x4* c) {
+    Frag x;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) x[r] = a[r] * w[0][r];
+#pragma unroll
+    for (int n = 0; n < N; ++n) c[n] = mma(x, b[n], c[n]);
+  }
+  static __device__ __forceinline__ void put4(float* p, f32x4 v) { *reinterpret_cast<f32x4*>(p) = v; }
+  static __device__ __forceinline__ uint32_t bad(uint4 u) {
+    const uint32_t q[4] = {u.x, u.y, u.z, u.w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m |= (uint32_t)((q[i] & 0x7f800000u) == 0x7f800000u) << i;
+    return m;
+  }
+};
+
+// decay^e for e >= 0, from l = log2(decay) (decay 0: l = -inf)
+__device__ __forceinline__ float decay_pow(float l, int e) { return e == 0 ? 1.f : exp2f(l * (float)e); }
+
+// What a workgroup holds: VS columns of the output and of the state (a
+// slice), the state's DK rows spread over the four waves.
+template <class T, int DK, int VS>
+struct Shape {
+  using M = Mat<T>;
+  static constexpr int kMT = DK / 16, kNT = VS / 16;          // the state's tiles
+  static constexpr int kWM = kMT < 4 ? kMT : 4, kWN = 4 / kWM;  // waves along each
+  static constexpr int kMW = kMT / kWM, kNW = kNT / kWN;      // tiles per wave
+  // LDS pitches, in elements: rows of K and of the state's copy keep 16-byte
+  // pieces and spread a read's rows over the banks; rows of V are read four
+  // at a time in 8-byte pieces
+  static constexpr int kPK = DK + (DK == 128 && sizeof(T) == 2 ? 16 : 16 / (int)sizeof(T));
+  static constexpr int kPV = VS + 4;
+  static constexpr int kBytes = (kC * kPK + kC * kPV + VS * kPK) * (int)sizeof(T) + (VS + 4) * 4;
+  static constexpr int kBlob = kMW * kNW * 4;  // state floats per thread
+  // column of the slice that index m of tile j stands for: a lane's tiles
+  // then hold VS / 4 consecutive columns of a row of the output
+  static __device__ __forceinline__ int column(int m, int j) { return (VS / 4) * (m >> 2) + 4 * j + (m & 3); }
+};
+
+// The state of a role in memory: this thread's elements.
+template <class T, int DK, int VS>
+struct State {
+  using Sh = Shape<T, DK, VS>;
+  f32x4 t[Sh::kMW][Sh::kNW];
+
+  static __device__ __forceinline__ int row(int i) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    return 16 * ((wave % Sh::kWM) * Sh::kMW + i) + 4 * (lane >> 4);
+  }
+  static __device__ __forceinline__ int tile(int j) { return (threadIdx.x >> 6) / Sh::kWM * Sh::kNW + j; }
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < Sh::kMW; ++i)
+#pragma unroll
+      for (int j = 0; j < Sh::kNW; ++j) t[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  // p: one head's [dk][dv] (flip: [dv][dk]) matrix
+  template <class F>
+  static __device__ __forceinline__ void each(int col0, int dk, int dv, F f) {
+#pragma unroll
+    for (int i = 0; i < Sh::kMW; ++i)
+#pragma unroll
+      for (int j = 0; j < Sh::kNW; ++j) {
+        const int r = row(i), c = col0 + Sh::column(threadIdx.x & 15, tile(j));
+        if (r < dk && c < dv) f(i, j, r, c);
+      }
+  }
+  __device__ __forceinline__ void load(const float* p, bool flip, int col0, int dk, int dv) {
+    clear();
+    each(col0, dk, dv, [&](int i, int j, int r, int c) {
+      if (flip) t[i][j] = *reinterpret_cast<const f32x4*>(p + (int64_t)c * dk + r);
+      else
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t[i][j][e] = p[(r + e) * dv + c];
+    });
+  }
+  __device__ __forceinline__ void store(float* p, bool flip, int col0, int dk, int dv) const {
+    each(col0, dk, dv, [&](int i, int j, int r, int c) {
+      if (flip) *reinterpret_cast<f32x4*>(p + (int64_t)c * dk + r) = t[i][j];
+      else
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[(r + e) * dv + c] = t[i][j][e];
+    });
+  }
+  // a segment's state in the workspace: 16 bytes per thread and tile
+  __device__ __forceinline__ void load_blob(const float* p) {
+#pragma unroll
+    for (int i = 0; i < Sh::kMW; ++i)
+#pragma unroll
+      for (int j = 0; j < Sh::kNW; ++j)
+        t[i][j] = reinterpret_cast<const f32x4*>(p)[(i * Sh::kNW + j) * kThreads + threadIdx.x];
+  }
+  __device__ __forceinline__ void store_blob(float* p) const {
+#pragma unroll
+    for (int i = 0; i < Sh::kMW; ++i)
+#pragma unroll
+      for (int j = 0; j < Sh::kNW; ++j)
+        reinterpret_cast<f32x4*>(p)[(i * Sh::kNW + j) * kThreads + threadIdx.x] = t[i][j];
+  }
+};
+
+// The work of a launch: units (history, head, segment) x (slice, role).
+struct Plan {
+  const int64_t* offsets;
+  const float* decay;
+  float* blobs;     // segments > 1: a state per (segment, slice and role, history and head)
+  int64_t units;    // B * H
+  int H, slices, inner;  // inner = slices * roles
+  int segments;
+  int64_t seg_len;  // rows per segment, a multiple of kC
+  Roles roles;
+};
+// The slices and roles of a unit read the same rows: they are eight blocks
+// apart, on one XCD and next to each other in time.
+__device__ __forceinline__ bool locate(const Plan& p, int64_t units, int64_t* unit, int* in) {
+  const int64_t b = blockIdx.x, span = 8 * (int64_t)p.inner;
+  *unit = b / span * 8 + (b & 7);
+  *in = (int)((b % span) >> 3);
+  return *unit < units;
+}
+
+// One workgroup: a slice of one segment of a history and head, chunk by
+// chunk.  Of a chunk's 64 rows each wave takes 16 (as N, so a lane holds one
+// row of the output):
+//   out = (q S) decay^(t + lead) + sum over i <= t of decay^(t - i) (q.k_i) v_i
+// and DK / 4 rows of the state:
+//   S <- decay^rows S + (k decay^(rows - 1 - i + 1 - lead))^T v
+// K and V of the next chunk are on their way to registers meanwhile; q goes
+// from memory straight to fragments.  ONLY_STATE: only S, from zero.
+template <class T, int DK, int VS, bool ONLY_STATE>
+__global__ __launch_bounds__(kThreads) void linattn_kernel(Plan plan) {
+  using M = Mat<T>;
+  using Sh = Shape<T, DK, VS>;
+  using Frag = typename M::Frag;
+  constexpr int PK = Sh::kPK, PV = Sh::kPV, NT = Sh::kNT, E = M::kPiece;
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  T* Ks = reinterpret_cast<T*>(smem);
+  T* Vs = Ks + kC * PK;
+  T* Ss = Vs + kC * PV;
+  int* first_bad = reinterpret_cast<int*>(Ss + VS * PK);  // per column, and any: [VS]
+
+  const int segs = ONLY_STATE ? plan.segments - 1 : plan.segments;
+  int64_t unit;
+  int in;
+  if (!locate(plan, plan.units * segs, &unit, &in)) return;
+  const int64_t bh = unit / segs;
+  const int seg = (int)(unit - bh * segs);
+  const int64_t b = bh / plan.H;
+  const int h = (int)(bh - b * plan.H);
+  const Role& role = plan.roles.r[in / plan.slices];
+  const int col0 = in % plan.slices * VS;
+  const int64_t beg = plan.offsets[b], len = plan.offsets[b + 1] - beg;
+  const int64_t s0 = seg * plan.seg_len;
+  if (seg > 0 && s0 >= len) return;
+  const bool ends = plan.segments == 1 || s0 + plan.seg_len >= len;  // the history's last segment
+  if (ONLY_STATE && ends) return;
+  const int64_t s1 = ends ? len : s0 + plan.seg_len;
+  const int64_t blob = ((int64_t)bh * plan.segments + seg) * plan.inner + in;
+  constexpr int64_t kBlobFloats = (int64_t)Sh::kBlob * kThreads;
+  const int dk = role.dk, dv = role.dv, lead = role.back ? 0 : 1;
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 15, g = lane >> 4;
+  State<T, DK, VS> S;
+  if (ONLY_STATE) S.clear();
+  else if (plan.segments > 1) S.load_blob(plan.blobs + blob * kBlobFloats);
+  else if (role.first) S.load(role.first + bh * dk * dv, role.flip, col0, dk, dv);
+  else S.clear();
+
+  // row t of the segment's time, in memory
+  const int64_t base = role.back ? beg + len - 1 : beg;
+  const int64_t dir = role.back ? -1 : 1;
+  const T* kp = static_cast<const T*>(role.k.p) + h * role.k.hs;
+  const T* vp = static_cast<const T*>(role.v.p) + h * role.v.hs + col0;
+  const T* qp = static_cast<const T*>(role.q.p) + h * role.q.hs;
+  T* op = static_cast<T*>(const_cast<void*>(role.o.p)) + h * role.o.hs + col0;
+
+  // a thread's pieces of a chunk of K and V
+  constexpr int KP = DK / E, VP = VS / E;                              // pieces per row
+  constexpr int KN = kC * KP / kThreads, VN = kC * VP / kThreads;      // per thread
+  uint4 kreg[KN], vreg[VN];
+  auto fetch = [&](int64_t c0) {
+    const int64_t left = s1 - c0;
+#pragma unroll
+    for (int i = 0; i < KN; ++i) {
+      const int e = i * kThreads + tid, r = e / KP, c = e % KP * E;
+      kreg[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < left && c < dk) kreg[i] = *reinterpret_cast<const uint4*>(kp + (base + dir * (c0 + r)) * role.k.ts + c);
+    }
+#pragma unroll
+    for (int i = 0; i < VN; ++i) {
+      const int e = i * kThreads + tid, r = e / VP, c = e % VP * E;
+      vreg[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < left && col0 + c < dv)
+        vreg[i] = *reinterpret_cast<const uint4*>(vp + (base + dir * (c0 + r)) * role.v.ts + c);
+    }
+  };
+  constexpr int QN = DK / M::kWide;
+  Frag qf[QN];
+  auto fetch_q = [&](int64_t c0) {
+    const int64_t t = c0 + 16 * wave + n;
+#pragma unroll
+    for (int f = 0; f < QN; ++f) {
+      const int c = f * M::kWide + g * (M::kWide / 4);
+      qf[f] = M::zero();
+      if (t < s1 && c < dk) qf[f] = *reinterpret_cast<const Frag*>(qp + (base + dir * t) * role.q.ts + c);
+    }
+  };
+
+  // weights that every full chunk shares
+  const float l2 = log2f(plan.decay[h]);
+  const float kscale = role.kscale;
+  f32x4 near[2];  // of the tile on the diagonal (0 above it) and of the one before it
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int e = n - 4 * g - r;
+    near[0][r] = e >= 0 ? kscale * decay_pow(l2, e) : 0.f;
+    near[1][r] = kscale * decay_pow(l2, 16 + e);
+  }
+  const float d16 = decay_pow(l2, 16);
+  const float from_state = decay_pow(l2, 16 * wave + n + lead);
+  f32x4 to_end[4];
+  int rows = 0;  // rows of the chunk that to_end stands for
+  auto weights = [&](int m) {
+    rows = m;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int e = m - lead - (16 * i + 4 * g + r);
+        to_end[i][r] = e >= 0 ? kscale * decay_pow(l2, e) : 0.f;
+      }
+  };
+  weights(kC);
+
+  if (s0 < s1) {
+    fetch(s0);
+    if (!ONLY_STATE) fetch_q(s0);
+  }
+  for (int64_t c0 = s0; c0 < s1; c0 += kC) {
+    const int m = (int)(s1 - c0 < kC ? s1 - c0 : kC);
+    __syncthreads();  // every wave is done with the chunk before
+    if (tid < VS + 4) first_bad[tid] = kC;
+#pragma unroll
+    for (int i = 0; i < KN; ++i) {
+      const int e = i * kThreads + tid;
+      *reinterpret_cast<uint4*>(Ks + e / KP * PK + e % KP * E) = kreg[i];
+    }
+    uint32_t bad = 0;
+#pragma unroll
+    for (int i = 0; i < VN; ++i) {
+      const int e = i * kThreads + tid;
+      uint2* p = reinterpret_cast<uint2*>(Vs + e / VP * PV + e % VP * E);
+      p[0] = make_uint2(vreg[i].x, vreg[i].y);
+      p[1] = make_uint2(vreg[i].z, vreg[i].w);
+      bad |= M::bad(vreg[i]);
+    }
+    if (!ONLY_STATE) {
+#pragma unroll
+      for (int i = 0; i < Sh::kMW; ++i)
+#pragma unroll
+        for (int j = 0; j < Sh::kNW; ++j)
+          M::put4(Ss + (16 * S.tile(j) + n) * PK + S.row(i), S.t[i][j]);
+    }
+    // a v that is not finite would reach rows before it as 0 * v: it goes
+    // into the products as zero, and its column is NaN from its row on
+    const bool any_bad = __syncthreads_or(bad != 0);
+    if (any_bad) {
+#pragma unroll
+      for (int i = 0; i < VN; ++i) {
+        const int e = i * kThreads + tid;
+        const uint32_t which = M::bad(vreg[i]);
+        for (int x = 0; x < E; ++x)
+          if ((which >> x) & 1u) {
+            Vs[e / VP * PV + e % VP * E + x] = 0;
+            atomicMin(&first_bad[e % VP * E + x], e / VP);
+          }
+      }
+      __syncthreads();
+    }
+    if (c0 + kC < s1) fetch(c0 + kC);
+
+    f32x4 out[NT];
+    f32x4 p[4];
+    if (!ONLY_STATE) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j) out[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int f = 0; f < QN; ++f)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) out[j] = M::mma(M::wide(Ss + (16 * j + n) * PK + f * M::kWide, g), qf[f], out[j]);
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) out[j][r] *= from_state;
+      float far = 1.f;
+#pragma unroll
+      for (int i = 3; i >= 0; --i) {
+        p[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (i > wave) continue;  // above the diagonal
+#pragma unroll
+        for (int f = 0; f < QN; ++f) p[i] = M::mma(M::wide(Ks + (16 * i + n) * PK + f * M::kWide, g), qf[f], p[i]);
+        if (i == wave) {
+          // selected, not multiplied: a masked product may not be finite
+#pragma unroll
+          for (int r = 0; r < 4; ++r) p[i][r] = n >= 4 * g + r ? p[i][r] * near[0][r] : 0.f;
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) p[i][r] *= near[1][r] * far;
+          far *= d16;
+        }
+      }
+      if (c0 + kC < s1) fetch_q(c0 + kC);
+    }
+    if (m != rows) weights(m);
+    const float all = decay_pow(l2, m);
+#pragma unroll
+    for (int i = 0; i < Sh::kMW; ++i)
+#pragma unroll
+      for (int j = 0; j < Sh::kNW; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) S.t[i][j][r] *= all;
+
+#pragma unroll
+    for (int f = 0; f < 4 / M::kTiles; ++f) {  // the chunk's rows, a fragment at a time
+      Frag vf[NT];
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        vf[j] = M::template time<PV>(Vs, f, lane, M::time_col(lane, VS / 4) + 4 * j);
+      if (!ONLY_STATE && f * M::kTiles <= wave) {
+        const Frag pf = M::pack(p + f * M::kTiles);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) out[j] = M::mma(vf[j], pf, out[j]);
+      }
+#pragma unroll
+      for (int i = 0; i < Sh::kMW; ++i) {
+        const int row0 = 16 * ((wave % Sh::kWM) * Sh::kMW + i);
+        const Frag kf = M::template time<PK>(Ks, f, lane, row0 + M::time_col(lane, 4));
+        if constexpr (Sh::kWN == 1) {
+          M::template mma_scaled<Sh::kNW>(kf, to_end + f * M::kTiles, vf, S.t[i]);
+        } else {
+          Frag vw[Sh::kNW];
+#pragma unroll
+          for (int j = 0; j < Sh::kNW; ++j)
+            vw[j] = M::template time<PV>(Vs, f, lane, M::time_col(lane, VS / 4) + 4 * S.tile(j));
+          M::template mma_scaled<Sh::kNW>(kf, to_end + f * M::kTiles, vw, S.t[i]);
+        }
+      }
+    }
+    const float nan = __uint_as_float(0x7fc00000u);
+    if (any_bad) {
+#pragma unroll
+      for (int i = 0; i < Sh::kMW; ++i)
+#pragma unroll
+        for (int j = 0; j < Sh::kNW; ++j)
+          if (first_bad[Sh::column(n, S.tile(j))] < kC) S.t[i][j] = f32x4{nan, nan, nan, nan};
+    }
+    if (!ONLY_STATE) {
+      const int64_t t = c0 + 16 * wave + n;
+      if (t < s1) {
+        float o[VS / 4];
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            o[4 * j + r] = out[j][r] * role.oscale;
+            if (any_bad && first_bad[(VS / 4) * g + 4 * j + r] <= 16 * wave + n) o[4 * j + r] = nan;
+          }
+        T* row = op + (base + dir * t) * role.o.ts;
+#pragma unroll
+        for (int x = 0; x < VS / 4; x += 4)
+          if (col0 + (VS / 4) * g + x < dv) M::put4(row + (VS / 4) * g + x, f32x4{o[x], o[x + 1], o[x + 2], o[x + 3]});
+      }
+    }
+  }
+  if (ONLY_STATE) S.store_blob(plan.blobs + blob * kBlobFloats);
+  else if (ends && role.last) S.store(role.last + bh * dk * dv, role.flip, col0, dk, dv);
+}
+
+// The states that enter the segments, in place of those that the segments
+// made from zero: in[s] = decay^seg_len in[s - 1] + made[s - 1].
+template <class T, int DK, int VS>
+__global__ __launch_bounds__(kThreads) void linattn_scan_kernel(Plan plan) {
+  using Sh = Shape<T, DK, VS>;
+  constexpr int64_t kBlobFloats = (int64_t)Sh::kBlob * kThreads;
+  int64_t bh;
+  int in;
+  if (!locate(plan, plan.units, &bh, &in)) return;
+  const int64_t b = bh / plan.H;
+  const int h = (int)(bh - b * plan.H);
+  const Role& role = plan.roles.r[in / plan.slices];
+  const int64_t len = plan.offsets[b + 1] - plan.offsets[b];
+  const float l2 = log2f(plan.decay[h]);
+  const float all = exp2f(l2 * (float)plan.seg_len);
+  State<T, DK, VS> S, made;
+  if (role.first) S.load(role.first + bh * role.dk * role.dv, role.flip, in % plan.slices * VS, role.dk, role.dv);
+  else S.clear();
+  for (int seg = 0; seg < plan.segments && (seg == 0 || seg * plan.seg_len < len); ++seg) {
+    float* p = plan.blobs + ((bh * plan.segments + seg) * plan.inner + in) * kBlobFloats;
+    const bool more = (seg + 1) * plan.seg_len < len;
+    if (more) made.load_blob(p);
+    S.store_blob(p);
+    if (!more) break;
+#pragma unroll
+    for (int i = 0; i < Sh::kMW; ++i)
+#pragma unroll
+      for (int j = 0; j < Sh::kNW; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) S.t[i][j][r] = S.t[i][j][r] * all + made.t[i][j][r];
+  }
 }
 
 template <class T>
@@ -97,23 +594,114 @@ bool head_ok(int32_t w) { return w >= 8 && w <= 128 && w % 8 == 0; }
 bool strided_ok(const Strided& s) { return s.p && aligned16(s.p) && s.ts % 8 == 0 && s.hs % 8 == 0; }
 bool state_ok(const float* p) { return aligned16(p); }
 
+// the block counts stay below 2^31 (kWantGroups and six per unit)
+bool shape_ok(int64_t B, int32_t H, int64_t max_len, int32_t dk, int32_t dv) {
+  return B >= 1 && H >= 1 && max_len >= 0 && head_ok(dk) && head_ok(dv) && B <= 0x7fffffffLL / 32 / H;
+}
+
 // shared by the forward and backward calls
 int check_shape(int32_t dtype, const int64_t* offsets, int64_t B, int32_t H, int64_t max_len, int32_t dk, int32_t dv,
                 const float* decay) {
   if (!is_activation(dtype) || B < 1 || H < 1 || max_len < 0 || !head_ok(dk) || !head_ok(dv)) return DLRM_E_INVALID;
   if (!offsets || !decay) return DLRM_E_INVALID;
-  if (B > 0x7fffffffLL / 32 / H) return DLRM_E_UNSUPPORTED;
+  if (!shape_ok(B, H, max_len, dk, dv)) return DLRM_E_UNSUPPORTED;
   return DLRM_OK;
 }
 
-int launch(const Roles& roles, int count, int32_t dtype, const int64_t* offsets, int64_t B, int32_t H,
-           const float* decay, hipStream_t stream) {
-  const dim3 grid((unsigned)(B * H), (unsigned)count);
-  if (dtype == DLRM_F32)
-    hipLaunchKernelGGL((linattn_kernel<float>), grid, dim3(128), 0, stream, roles, offsets, H, decay);
-  else
-    hipLaunchKernelGGL((linattn_kernel<uint16_t>), grid, dim3(128), 0, stream, roles, offsets, H, decay);
+// the padded width of a contraction, and of a slice of the output
+int pad_width(int32_t w) { return w <= 32 ? 32 : w <= 64 ? 64 : 128; }
+int slice_width(int32_t w) { return w <= 32 ? 32 : 64; }
+
+// Segments of a launch: enough workgroups for the device from few long
+// histories, none shorter than kSegMin rows.
+constexpr int64_t kSegMin = 256;
+constexpr int64_t kWantGroups = 1024;
+void cut(int64_t groups, int64_t max_len, int* segments, int64_t* seg_len) {
+  int64_t want = groups > 0 ? kWantGroups / groups : 1;
+  const int64_t most = max_len / kSegMin;
+  want = want < most ? want : most;
+  if (want < 2) {
+    *segments = 1;
+    *seg_len = round_up(max_len > 0 ? max_len : 1, kC);
+    return;
+  }
+  *seg_len = round_up(ceil_div(max_len, want), kC);
+  *segments = (int)ceil_div(max_len, *seg_len);
+}
+
+// workspace of roles that share a contraction width and an output width
+size_t blob_bytes(int64_t units, int count, int64_t max_len, int32_t dk, int32_t dv) {
+  const int vs = slice_width(dv), slices = (int)ceil_div(dv, vs);
+  int segments;
+  int64_t seg_len;
+  cut(units * slices * count, max_len, &segments, &seg_len);
+  if (segments < 2) return 0;
+  return (size_t)units * segments * slices * count * pad_width(dk) * vs * 4;
+}
+
+template <class T, int DK, int VS>
+int launch_shape(const Plan& plan, hipStream_t stream) {
+  constexpr int lds = Shape<T, DK, VS>::kBytes;
+  // more than 64 KB of LDS has to be asked for, once per device
+  if (lds > 64 * 1024) {
+    static bool done[kMaxDevices] = {};
+    const int dev = current_device();
+    if (!done[dev]) {
+      const void* f[2] = {reinterpret_cast<const void*>(&linattn_kernel<T, DK, VS, false>),
+                          reinterpret_cast<const void*>(&linattn_kernel<T, DK, VS, true>)};
+      for (const void* k : f) {
+        const hipError_t e = hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+        if (e != hipSuccess) {
+          g_last_hip_error = (int)e;
+          return DLRM_E_HIP;
+        }
+      }
+      done[dev] = true;
+    }
+  }
+  auto blocks = [&](int64_t units) { return dim3((unsigned)(ceil_div(units, 8) * 8 * plan.inner)); };
+  if (plan.segments > 1) {
+    hipLaunchKernelGGL((linattn_kernel<T, DK, VS, true>), blocks(plan.units * (plan.segments - 1)), dim3(kThreads), lds,
+                       stream, plan);
+    hipLaunchKernelGGL((linattn_scan_kernel<T, DK, VS>), blocks(plan.units), dim3(kThreads), 0, stream, plan);
+  }
+  hipLaunchKernelGGL((linattn_kernel<T, DK, VS, false>), blocks(plan.units * plan.segments), dim3(kThreads), lds, stream,
+                     plan);
   return launch_status();
+}
+
+template <class T>
+int launch_type(const Plan& plan, hipStream_t stream) {
+  const int dk = pad_width(plan.roles.r[0].dk), vs = slice_width(plan.roles.r[0].dv);
+  if (vs == 32) {
+    if (dk == 32) return launch_shape<T, 32, 32>(plan, stream);
+    if (dk == 64) return launch_shape<T, 64, 32>(plan, stream);
+    return launch_shape<T, 128, 32>(plan, stream);
+  }
+  if (dk == 32) return launch_shape<T, 32, 64>(plan, stream);
+  if (dk == 64) return launch_shape<T, 64, 64>(plan, stream);
+  return launch_shape<T, 128, 64>(plan, stream);
+}
+
+// Roles of the same widths, one launch (or three, where histories are cut).
+int launch(const Role* roles, int count, int32_t dtype, const int64_t* offsets, int64_t B, int32_t H, int64_t max_len,
+           const float* decay, void* ws, hipStream_t stream) {
+  Plan p{};
+  p.offsets = offsets;
+  p.decay = decay;
+  p.blobs = static_cast<float*>(ws);
+  p.units = B * H;
+  p.H = H;
+  p.slices = (int)ceil_div(roles[0].dv, slice_width(roles[0].dv));
+  p.inner = p.slices * count;
+  cut(p.units * p.inner, max_len, &p.segments, &p.seg_len);
+  for (int i = 0; i < count; ++i) p.roles.r[i] = roles[i];
+  return dtype == DLRM_F32 ? launch_type<float>(p, stream) : launch_type<uint16_t>(p, stream);
+}
+
+// Whether the backward pass's three roles fit one launch: equal padded widths
+bool one_launch(int32_t dk, int32_t dv) {
+  return pad_width(dk) == pad_width(dv) && slice_width(dk) == slice_width(dv);
 }
 
 }  // namespace
@@ -122,8 +710,8 @@ int launch(const Roles& roles, int count, int32_t dtype, const int64_t* offsets,
 using namespace dlrm;
 
 extern "C" size_t dlrm_linattn_workspace_size(int64_t B, int32_t H, int64_t max_len, int32_t dk, int32_t dv) {
-  (void)B; (void)H; (void)max_len; (void)dk; (void)dv;
-  return 0;
+  if (!shape_ok(B, H, max_len, dk, dv)) return 0;
+  return blob_bytes(B * H, 1, max_len, dk, dv);
 }
 
 extern "C" int dlrm_linattn_fwd(const void* q, int64_t q_ts, int64_t q_hs, const void* k, int64_t k_ts, int64_t k_hs,
@@ -131,7 +719,6 @@ extern "C" int dlrm_linattn_fwd(const void* q, int64_t q_ts, int64_t q_hs, const
                                 int64_t B, int32_t H, int64_t max_len, int32_t dk, int32_t dv, const float* decay,
                                 float scale, const float* state0, void* o, int64_t o_ts, int64_t o_hs, float* state,
                                 void* ws, size_t ws_bytes, hipStream_t stream) {
-  (void)ws_bytes;
   if (reinterpret_cast<uintptr_t>(ws) & 255u) return DLRM_E_INVALID;
   const int rc = check_shape(dtype, offsets, B, H, max_len, dk, dv, decay);
   if (rc != DLRM_OK) return rc;
@@ -140,14 +727,17 @@ extern "C" int dlrm_linattn_fwd(const void* q, int64_t q_ts, int64_t q_hs, const
   if (max_len > 0 && (!strided_ok(r.q) || !strided_ok(r.k) || !strided_ok(r.v) || !strided_ok(r.o)))
     return DLRM_E_INVALID;
   if (!state_ok(state0) || !state_ok(state)) return DLRM_E_INVALID;
-  Roles roles{};
-  roles.r[0] = r;
-  return launch(roles, 1, dtype, offsets, B, H, decay, stream);
+  const size_t need = dlrm_linattn_workspace_size(B, H, max_len, dk, dv);
+  if (need > 0 && (!ws || ws_bytes < need)) return DLRM_E_WORKSPACE;
+  return launch(&r, 1, dtype, offsets, B, H, max_len, decay, ws, stream);
 }
 
 extern "C" size_t dlrm_linattn_bwd_workspace_size(int64_t B, int32_t H, int64_t max_len, int32_t dk, int32_t dv) {
-  (void)B; (void)H; (void)max_len; (void)dk; (void)dv;
-  return 0;
+  if (!shape_ok(B, H, max_len, dk, dv)) return 0;
+  if (one_launch(dk, dv)) return blob_bytes(B * H, 3, max_len, dv, dk);
+  // one after the other on the same workspace
+  const size_t two = blob_bytes(B * H, 2, max_len, dv, dk), one = blob_bytes(B * H, 1, max_len, dk, dv);
+  return two > one ? two : one;
 }
 
 extern "C" int dlrm_linattn_bwd(const void* q, int64_t q_ts, int64_t q_hs, const void* k, int64_t k_ts, int64_t k_hs,
@@ -157,7 +747,6 @@ extern "C" int dlrm_linattn_bwd(const void* q, int64_t q_ts, int64_t q_hs, const
                                 const float* state0, const float* dstate, void* dq, int64_t dq_ts, int64_t dq_hs,
                                 void* dk_, int64_t dk_ts, int64_t dk_hs, void* dv_, int64_t dv_ts, int64_t dv_hs,
                                 float* dstate0, void* ws, size_t ws_bytes, hipStream_t stream) {
-  (void)ws_bytes;
   if (reinterpret_cast<uintptr_t>(ws) & 255u) return DLRM_E_INVALID;
   const int rc = check_shape(dtype, offsets, B, H, max_len, dk, dv, decay);
   if (rc != DLRM_OK) return rc;
@@ -168,11 +757,15 @@ extern "C" int dlrm_linattn_bwd(const void* q, int64_t q_ts, int64_t q_hs, const
       if (!strided_ok(*s)) return DLRM_E_INVALID;
   if (!state_ok(state0) || !state_ok(dstate) || !state_ok(dstate0) || (dstate0 && dstate0 == dstate))
     return DLRM_E_INVALID;
-  Roles roles{};
-  roles.r[0] = Role{O, V, K, DQ, state0, nullptr, dv, dk, 1, 0, 1.f, scale};
-  roles.r[1] = Role{V, O, Q, DK, dstate, nullptr, dv, dk, 1, 1, scale, 1.f};
-  roles.r[2] = Role{K, Q, O, DV, dstate, dstate0, dk, dv, 0, 1, scale, 1.f};
-  return launch(roles, 3, dtype, offsets, B, H, decay, stream);
+  const size_t need = dlrm_linattn_bwd_workspace_size(B, H, max_len, dk, dv);
+  if (need > 0 && (!ws || ws_bytes < need)) return DLRM_E_WORKSPACE;
+  const Role roles[3] = {Role{O, V, K, DQ, state0, nullptr, dv, dk, 1, 0, 1.f, scale},
+                         Role{V, O, Q, DK, dstate, nullptr, dv, dk, 1, 1, scale, 1.f},
+                         Role{K, Q, O, DV, dstate, dstate0, dk, dv, 0, 1, scale, 1.f}};
+  if (one_launch(dk, dv)) return launch(roles, 3, dtype, offsets, B, H, max_len, decay, ws, stream);
+  const int first = launch(roles, 2, dtype, offsets, B, H, max_len, decay, ws, stream);
+  if (first != DLRM_OK) return first;
+  return launch(roles + 2, 1, dtype, offsets, B, H, max_len, decay, ws, stream);
 }
 
 extern "C" int dlrm_linattn_step(const void* q, int64_t q_bs, int64_t q_hs, const void* k, int64_t k_bs, int64_t k_hs,
