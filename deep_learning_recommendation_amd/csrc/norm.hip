@@ -14,143 +14,469 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxD = 16384;
 
-// sum (or maximum) over the block's threads, in a fixed order
-template <class Op>
-__device__ __forceinline__ float block_reduce(float v, float* s, Op op) {
+// A pass over n rows of d elements, one group of LPR lanes per row (LPR up to
+// a wave; or the whole block, kThreads), NP pieces of VE elements per lane:
+// lane l's piece i holds columns (i LPR + l) VE ...  A row is read once, and
+// its sums run over the lanes' registers in a fixed order.
+template <int LPR>
+struct Group {
+  static constexpr int kPerBlock = LPR >= kThreads ? 1 : kThreads / LPR;
+  static __device__ __forceinline__ int lane() { return threadIdx.x & (LPR - 1); }
+  static __device__ __forceinline__ int index() { return threadIdx.x / LPR; }
+  template <class V, class Op>
+  static __device__ __forceinline__ V reduce(V v, Op op) {
 #pragma unroll
-  for (int o = 1; o < 64; o <<= 1) v = op(v, __shfl_xor(v, o, 64));
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
-  __syncthreads();
-  v = s[0];
+    for (int o = 1; o < (LPR < 64 ? LPR : 64); o <<= 1) v = op(v, __shfl_xor(v, o, 64));
+    if constexpr (LPR > 64) {
+      __shared__ V s[kThreads / 64];
+      __syncthreads();
+      if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
+      __syncthreads();
+      v = s[0];
 #pragma unroll
-  for (int w = 1; w < kThreads / 64; ++w) v = op(v, s[w]);
-  return v;
-}
-struct Add {
-  __device__ float operator()(float a, float b) const { return a + b; }
+      for (int w = 1; w < kThreads / 64; ++w) v = op(v, s[w]);
+    }
+    return v;
+  }
 };
-struct Max {
-  __device__ float operator()(float a, float b) const { return fmaxf(a, b); }
+struct Add {
+  __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
+};
+struct Top {
+  __device__ __forceinline__ uint32_t operator()(uint32_t a, uint32_t b) const { return a > b ? a : b; }
 };
 
+// an output piece: the activation type, or int8 bytes
+template <class TY, int VE>
+struct Out {
+  static __device__ __forceinline__ void store(TY* p, const float (&v)[VE]) {
+    Piece<TY, VE> o;
+    o.set(v);
+    o.store(p);
+  }
+};
+template <int VE>
+struct Out<int8_t, VE> {
+  static __device__ __forceinline__ void store(int8_t* p, const float (&v)[VE]) {
+    uint32_t w[VE / 4];
+#pragma unroll
+    for (int i = 0; i < VE / 4; ++i) {
+      w[i] = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[i] |= ((uint32_t)(int)v[4 * i + j] & 0xffu) << (8 * j);
+    }
+    if constexpr (VE == 8) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t*>(p) = w[0];
+  }
+};
+
+// bit j: element e + j is kept (VE of them, e a multiple of VE, VE divides 8)
+template <int VE>
+__device__ __forceinline__ uint32_t keep_piece(const DropState& st, int64_t e, uint32_t cut) {
+  const uint32_t m = keep8(st, (uint64_t)(e >> 3), cut);
+  return VE == 8 ? m : m >> (e & 7);
+}
+
+struct Fwd {
+  const void *x, *res;
+  int64_t x_ld, res_ld;
+  const float* w;
+  int64_t n;
+  int d;
+  float eps;
+  uint32_t cut;
+  float factor;
+  const int64_t* rng;
+  void *h, *y;
+  int64_t h_ld, y_ld;
+  float *scale_bias, *rstd;
+};
+
+template <class T, class TY, int VE, int LPR, int NP>
+__global__ __launch_bounds__(kThreads) void addnorm_fwd_kernel(Fwd a) {
+  using G = Group<LPR>;
+  const DropState st = a.cut ? drop_state(a.rng) : DropState{0, 0};
+  const T *x = static_cast<const T*>(a.x), *res = static_cast<const T*>(a.res);
+  T* h = static_cast<T*>(a.h);
+  TY* y = static_cast<TY*>(a.y);
+  float w[NP][VE];
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    const int c = (i * LPR + G::lane()) * VE;
+#pragma unroll
+    for (int j = 0; j < VE; ++j) w[i][j] = 0.f;
+    if (c < a.d) {
+      Piece<float, VE> p;
+      p.load(a.w + c);
+      p.get(w[i]);
+    }
+  }
+  // (a group larger than a wave steps with its whole block)
+  for (int64_t row = (int64_t)blockIdx.x * G::kPerBlock + G::index(); row < a.n;
+       row += (int64_t)gridDim.x * G::kPerBlock) {
+    Piece<T, VE> px[NP], pr[NP];
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int c = (i * LPR + G::lane()) * VE;
+      if (c < a.d) {
+        px[i].load(x + row * a.x_ld + c);
+        if (res) pr[i].load(res + row * a.res_ld + c);
+      }
+    }
+    float v[NP][VE];
+    float sq = 0.f;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int c = (i * LPR + G::lane()) * VE;
+#pragma unroll
+      for (int j = 0; j < VE; ++j) v[i][j] = 0.f;
+      if (c >= a.d) continue;
+      px[i].get(v[i]);
+      if (a.cut) {
+        const uint32_t keep = keep_piece<VE>(st, row * a.d + c, a.cut);
+#pragma unroll
+        for (int j = 0; j < VE; ++j) v[i][j] = (keep >> j) & 1u ? v[i][j] : 0.f;
+      }
+      float r[VE];
+#pragma unroll
+      for (int j = 0; j < VE; ++j) r[j] = 0.f;
+      if (res) pr[i].get(r);
+      // the factor's product and the addition round once
+#pragma unroll
+      for (int j = 0; j < VE; ++j) {
+        v[i][j] = __builtin_fmaf(v[i][j], a.factor, r[j]);
+        sq = __builtin_fmaf(v[i][j], v[i][j], sq);
+      }
+      if (h) Out<T, VE>::store(h + row * a.h_ld + c, v[i]);
+    }
+    const float r = 1.f / sqrtf(G::reduce(sq, Add()) / (float)a.d + a.eps);
+    if (a.rstd && G::lane() == 0) a.rstd[row] = r;
+#pragma unroll
+    for (int i = 0; i < NP; ++i)
+#pragma unroll
+      for (int j = 0; j < VE; ++j) v[i][j] = v[i][j] * r * w[i][j];
+    if constexpr (sizeof(TY) == 1) {
+      // magnitudes compared as bits: a NaN is the largest
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < NP; ++i)
+        if ((i * LPR + G::lane()) * VE < a.d) {
+#pragma unroll
+          for (int j = 0; j < VE; ++j) top = Top()(top, __float_as_uint(v[i][j]) & 0x7fffffffu);
+        }
+      top = G::reduce(top, Top());
+      const float unit = __uint_as_float(top) / 127.f;
+      const float inv = unit > 0.f ? 1.f / unit : 0.f;
+      if (G::lane() == 0) *reinterpret_cast<float2*>(a.scale_bias + 2 * row) = make_float2(unit, 0.f);
+#pragma unroll
+      for (int i = 0; i < NP; ++i)
+#pragma unroll
+        for (int j = 0; j < VE; ++j) v[i][j] = unit > 0.f ? rintf(v[i][j] * inv) : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int c = (i * LPR + G::lane()) * VE;
+      if (c < a.d) Out<TY, VE>::store(y + row * a.y_ld + c, v[i]);
+    }
+  }
+}
+
+struct Bwd {
+  const void *dy, *dh, *h;
+  int64_t dy_ld, dh_ld, h_ld;
+  const float *w, *rstd;
+  int64_t n;
+  int d;
+  uint32_t cut;
+  float factor;
+  const int64_t* rng;
+  void *dx, *dres;
+  int64_t dx_ld, dres_ld;
+  float* part;
+};
+
+template <class T, int VE, int LPR, int NP>
+__global__ __launch_bounds__(kThreads) void addnorm_bwd_kernel(Bwd a) {
+  using G = Group<LPR>;
+  const DropState st = a.cut ? drop_state(a.rng) : DropState{0, 0};
+  const T *dy = static_cast<const T*>(a.dy), *dh = static_cast<const T*>(a.dh), *h = static_cast<const T*>(a.h);
+  T *dx = static_cast<T*>(a.dx), *dres = static_cast<T*>(a.dres);
+  float w[NP][VE], dw[NP][VE];
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    const int c = (i * LPR + G::lane()) * VE;
+#pragma unroll
+    for (int j = 0; j < VE; ++j) w[i][j] = dw[i][j] = 0.f;
+    if (c < a.d) {
+      Piece<float, VE> p;
+      p.load(a.w + c);
+      p.get(w[i]);
+    }
+  }
+  for (int64_t row = (int64_t)blockIdx.x * G::kPerBlock + G::index(); row < a.n;
+       row += (int64_t)gridDim.x * G::kPerBlock) {
+    Piece<T, VE> py[NP], ph[NP], pd[NP];
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int c = (i * LPR + G::lane()) * VE;
+      if (c < a.d) {
+        py[i].load(dy + row * a.dy_ld + c);
+        ph[i].load(h + row * a.h_ld + c);
+        if (dh) pd[i].load(dh + row * a.dh_ld + c);
+      }
+    }
+    const float r = a.rstd[row];
+    float dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      if ((i * LPR + G::lane()) * VE >= a.d) continue;
+      float g[VE], v[VE];
+      py[i].get(g);
+      ph[i].get(v);
+#pragma unroll
+      for (int j = 0; j < VE; ++j) {
+        const float gv = g[j] * v[j];
+        dot = __builtin_fmaf(gv, w[i][j], dot);
+        dw[i][j] = __builtin_fmaf(gv, r, dw[i][j]);
+      }
+    }
+    const float k = G::reduce(dot, Add()) / (float)a.d * r * r * r;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int c = (i * LPR + G::lane()) * VE;
+      if (c >= a.d) continue;
+      float g[VE], v[VE], t[VE];
+      py[i].get(g);
+      ph[i].get(v);
+#pragma unroll
+      for (int j = 0; j < VE; ++j) t[j] = r * (g[j] * w[i][j]) - k * v[j];
+      if (dh) {
+        float u[VE];
+        pd[i].get(u);
+#pragma unroll
+        for (int j = 0; j < VE; ++j) t[j] += u[j];
+      }
+      if (dres) Out<T, VE>::store(dres + row * a.dres_ld + c, t);
+      if (dx) {
+        if (a.cut) {
+          const uint32_t keep = keep_piece<VE>(st, row * a.d + c, a.cut);
+#pragma unroll
+          for (int j = 0; j < VE; ++j) t[j] = (keep >> j) & 1u ? t[j] * a.factor : 0.f;
+        }
+        Out<T, VE>::store(dx + row * a.dx_ld + c, t);
+      }
+    }
+  }
+  // the block's groups added in order: lanes of a wave, then waves
+  float* part = a.part + (int64_t)blockIdx.x * a.d;
+  if constexpr (LPR >= kThreads) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int c = (i * LPR + G::lane()) * VE;
+      if (c < a.d) Out<float, VE>::store(part + c, dw[i]);
+    }
+  } else {
+    __shared__ float s[kThreads / 64][LPR * NP * VE];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int i = 0; i < NP; ++i)
+#pragma unroll
+      for (int j = 0; j < VE; ++j) {
+        float v = dw[i][j];
+#pragma unroll
+        for (int o = LPR; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
+        if (lane < LPR) s[wave][(i * LPR + lane) * VE + j] = v;
+      }
+    __syncthreads();
+    for (int c = threadIdx.x; c < a.d; c += kThreads) {
+      float v = s[0][c];
+#pragma unroll
+      for (int q = 1; q < kThreads / 64; ++q) v += s[q][c];
+      part[c] = v;
+    }
+  }
+}
+
+// dw[c] = the blocks' sums: 16 threads per column, each its blocks in order,
+// then the 16 in order
+constexpr int kDwCols = 16, kDwRows = kThreads / kDwCols;
+__global__ __launch_bounds__(kThreads) void dw_kernel(const float* __restrict__ part, int blocks, int d,
+                                                      float* __restrict__ dw) {
+  __shared__ float s[kDwRows][kDwCols];
+  const int col = threadIdx.x % kDwCols, slice = threadIdx.x / kDwCols;
+  const int c = blockIdx.x * kDwCols + col;
+  float v = 0.f;
+  if (c < d) {
+#pragma unroll 8
+    for (int b = slice; b < blocks; b += kDwRows) v += part[(int64_t)b * d + c];
+  }
+  s[slice][col] = v;
+  __syncthreads();
+  if (slice == 0 && c < d) {
+    v = s[0][col];
+#pragma unroll
+    for (int q = 1; q < kDwRows; ++q) v += s[q][col];
+    dw[c] = v;
+  }
+}
+
+// Rows that no piece fits (an odd width, or rows off their alignment): a
+// block per row, element by element, the row kept in LDS.
 __device__ __forceinline__ bool kept(const DropState& st, int64_t e, uint32_t cut) {
   return (keep8(st, (uint64_t)(e >> 3), cut) >> (e & 7)) & 1u;
 }
 
-// One block per row, element by element, h recomputed in each pass.
 template <class T, class TY>
-__global__ __launch_bounds__(kThreads) void addnorm_fwd_kernel(const T* x, int64_t x_ld, const T* res, int64_t res_ld,
-                                                               const float* __restrict__ w, int64_t n, int d,
-                                                               float eps, uint32_t cut, float factor,
-                                                               const int64_t* __restrict__ rng, T* h, int64_t h_ld,
-                                                               TY* y, int64_t y_ld, float* __restrict__ scale_bias,
-                                                               float* __restrict__ rstd) {
-  __shared__ float s[kThreads / 64];
-  __shared__ float hrow[kMaxD];
-  const DropState st = cut ? drop_state(rng) : DropState{0, 0};
-  for (int64_t row = blockIdx.x; row < n; row += gridDim.x) {
+__global__ __launch_bounds__(kThreads) void addnorm_fwd_odd_kernel(Fwd a) {
+  using G = Group<kThreads>;
+  extern __shared__ float hrow[];
+  const DropState st = a.cut ? drop_state(a.rng) : DropState{0, 0};
+  const T *x = static_cast<const T*>(a.x), *res = static_cast<const T*>(a.res);
+  T* h = static_cast<T*>(a.h);
+  TY* y = static_cast<TY*>(a.y);
+  for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x) {
     float sq = 0.f;
-    for (int c = threadIdx.x; c < d; c += kThreads) {
-      // the factor's product and the addition round once
-      float v = to_f32(x[row * x_ld + c]);
-      if (cut) v = kept(st, row * d + c, cut) ? v : 0.f;
-      v = __builtin_fmaf(v, factor, res ? to_f32(res[row * res_ld + c]) : 0.f);
+    for (int c = threadIdx.x; c < a.d; c += kThreads) {
+      float v = to_f32(x[row * a.x_ld + c]);
+      if (a.cut) v = kept(st, row * a.d + c, a.cut) ? v : 0.f;
+      v = __builtin_fmaf(v, a.factor, res ? to_f32(res[row * a.res_ld + c]) : 0.f);
       hrow[c] = v;
-      if (h) h[row * h_ld + c] = from_f32<T>(v);
-      sq += v * v;
+      if (h) h[row * a.h_ld + c] = from_f32<T>(v);
+      sq = __builtin_fmaf(v, v, sq);
     }
-    const float r = 1.f / sqrtf(block_reduce(sq, s, Add()) / (float)d + eps);
-    if (rstd && threadIdx.x == 0) rstd[row] = r;
+    const float r = 1.f / sqrtf(G::reduce(sq, Add()) / (float)a.d + a.eps);
+    if (a.rstd && threadIdx.x == 0) a.rstd[row] = r;
     if constexpr (sizeof(TY) == 1) {
-      float top = 0.f, nan = 0.f;
-      for (int c = threadIdx.x; c < d; c += kThreads) {
-        const float v = hrow[c] * r * w[c];
-        top = fmaxf(top, fabsf(v));
-        if (v != v) nan = 1.f;
-      }
-      top = block_reduce(top, s, Max());
-      nan = block_reduce(nan, s, Max());
-      const float unit = nan > 0.f ? __uint_as_float(0x7fc00000u) : top / 127.f;
+      uint32_t top = 0;
+      for (int c = threadIdx.x; c < a.d; c += kThreads)
+        top = Top()(top, __float_as_uint(hrow[c] * r * a.w[c]) & 0x7fffffffu);
+      top = G::reduce(top, Top());
+      const float unit = __uint_as_float(top) / 127.f;
+      const float inv = unit > 0.f ? 1.f / unit : 0.f;
       if (threadIdx.x == 0) {
-        scale_bias[2 * row] = unit;
-        scale_bias[2 * row + 1] = 0.f;
+        a.scale_bias[2 * row] = unit;
+        a.scale_bias[2 * row + 1] = 0.f;
       }
-      for (int c = threadIdx.x; c < d; c += kThreads) {
-        const float q = rintf(hrow[c] * r * w[c] / unit);
-        y[row * y_ld + c] = unit > 0.f ? (TY)fminf(fmaxf(q, -127.f), 127.f) : (TY)0;
-      }
+      for (int c = threadIdx.x; c < a.d; c += kThreads)
+        y[row * a.y_ld + c] = unit > 0.f ? (TY)rintf(hrow[c] * r * a.w[c] * inv) : (TY)0;
     } else {
-      for (int c = threadIdx.x; c < d; c += kThreads) y[row * y_ld + c] = from_f32<TY>(hrow[c] * r * w[c]);
+      for (int c = threadIdx.x; c < a.d; c += kThreads) y[row * a.y_ld + c] = from_f32<TY>(hrow[c] * r * a.w[c]);
     }
-    __syncthreads();
   }
 }
 
 template <class T>
-__global__ __launch_bounds__(kThreads) void addnorm_bwd_kernel(const T* dy, int64_t dy_ld, const T* dh, int64_t dh_ld,
-                                                               const T* __restrict__ h, int64_t h_ld,
-                                                               const float* __restrict__ w,
-                                                               const float* __restrict__ rstd, int64_t n, int d,
-                                                               uint32_t cut, float factor,
-                                                               const int64_t* __restrict__ rng, T* dx, int64_t dx_ld,
-                                                               T* dres, int64_t dres_ld, float* __restrict__ part) {
-  __shared__ float s[kThreads / 64];
-  __shared__ float dwrow[kMaxD];
-  const DropState st = cut ? drop_state(rng) : DropState{0, 0};
-  for (int c = threadIdx.x; c < d; c += kThreads) dwrow[c] = 0.f;
-  for (int64_t row = blockIdx.x; row < n; row += gridDim.x) {
-    const float r = rstd[row];
+__global__ __launch_bounds__(kThreads) void addnorm_bwd_odd_kernel(Bwd a) {
+  using G = Group<kThreads>;
+  extern __shared__ float dwrow[];
+  const DropState st = a.cut ? drop_state(a.rng) : DropState{0, 0};
+  const T *dy = static_cast<const T*>(a.dy), *dh = static_cast<const T*>(a.dh), *h = static_cast<const T*>(a.h);
+  T *dx = static_cast<T*>(a.dx), *dres = static_cast<T*>(a.dres);
+  for (int c = threadIdx.x; c < a.d; c += kThreads) dwrow[c] = 0.f;
+  for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x) {
+    const float r = a.rstd[row];
     float dot = 0.f;
-    for (int c = threadIdx.x; c < d; c += kThreads) {
-      const float gy = to_f32(dy[row * dy_ld + c]), hv = to_f32(h[row * h_ld + c]);
-      dot += gy * w[c] * hv;
-      dwrow[c] += gy * hv * r;
+    for (int c = threadIdx.x; c < a.d; c += kThreads) {
+      const float gv = to_f32(dy[row * a.dy_ld + c]) * to_f32(h[row * a.h_ld + c]);
+      dot = __builtin_fmaf(gv, a.w[c], dot);
+      dwrow[c] = __builtin_fmaf(gv, r, dwrow[c]);
     }
-    const float k = block_reduce(dot, s, Add()) / (float)d * r * r * r;
-    for (int c = threadIdx.x; c < d; c += kThreads) {
-      float t = r * (to_f32(dy[row * dy_ld + c]) * w[c]) - k * to_f32(h[row * h_ld + c]);
-      if (dh) t += to_f32(dh[row * dh_ld + c]);
-      const float tx = cut ? (kept(st, row * d + c, cut) ? t * factor : 0.f) : t;
-      if (dres) dres[row * dres_ld + c] = from_f32<T>(t);
-      if (dx) dx[row * dx_ld + c] = from_f32<T>(tx);
+    const float k = G::reduce(dot, Add()) / (float)a.d * r * r * r;
+    for (int c = threadIdx.x; c < a.d; c += kThreads) {
+      float t = r * (to_f32(dy[row * a.dy_ld + c]) * a.w[c]) - k * to_f32(h[row * a.h_ld + c]);
+      if (dh) t += to_f32(dh[row * a.dh_ld + c]);
+      const float tx = a.cut ? (kept(st, row * a.d + c, a.cut) ? t * a.factor : 0.f) : t;
+      if (dres) dres[row * a.dres_ld + c] = from_f32<T>(t);
+      if (dx) dx[row * a.dx_ld + c] = from_f32<T>(tx);
     }
   }
-  for (int c = threadIdx.x; c < d; c += kThreads) part[(int64_t)blockIdx.x * d + c] = dwrow[c];
+  for (int c = threadIdx.x; c < a.d; c += kThreads) a.part[(int64_t)blockIdx.x * a.d + c] = dwrow[c];
 }
 
-// dw[c] = the blocks' sums in block order
-__global__ __launch_bounds__(kThreads) void dw_kernel(const float* __restrict__ part, int blocks, int d,
-                                                      float* __restrict__ dw) {
-  const int c = blockIdx.x * kThreads + threadIdx.x;
-  if (c >= d) return;
-  float a = 0.f;
-  for (int b = 0; b < blocks; ++b) a += part[(int64_t)b * d + c];
-  dw[c] = a;
-}
-
+// Blocks of the backward pass, each with its own sums for dw: four per CU.
 constexpr int kBwdBlocks = 1024;
+constexpr int kFwdBlocks = 4096;
 
+// Lanes per row: a power of two that covers the row with one piece each, up
+// to a wave; up to four pieces per lane of a wave, then a block per row.
+#define DLRM_NORM_WIDTHS(CALL)                                   \
+  const int pieces = (d + VE - 1) / VE;                          \
+  if (pieces <= 2) return CALL(2, 1);                            \
+  if (pieces <= 4) return CALL(4, 1);                            \
+  if (pieces <= 8) return CALL(8, 1);                            \
+  if (pieces <= 16) return CALL(16, 1);                          \
+  if (pieces <= 32) return CALL(32, 1);                          \
+  if (pieces <= 64) return CALL(64, 1);                          \
+  if (pieces <= 128) return CALL(64, 2);                         \
+  if (pieces <= 256) return CALL(64, 4);                         \
+  if (pieces <= 512) return CALL(256, 2);                        \
+  if (pieces <= 1024) return CALL(256, 4);                       \
+  return CALL(256, 16384 / 256 / VE);
+
+template <class T, class TY, int VE, int LPR, int NP>
+int launch_fwd_width(const Fwd& a, hipStream_t stream) {
+  const int64_t blocks = ceil_div(a.n, Group<LPR>::kPerBlock);
+  hipLaunchKernelGGL((addnorm_fwd_kernel<T, TY, VE, LPR, NP>), dim3((unsigned)(blocks < kFwdBlocks ? blocks : kFwdBlocks)),
+                     dim3(kThreads), 0, stream, a);
+  return launch_status();
+}
+template <class T, class TY, int VE>
+int launch_fwd_pieces(const Fwd& a, hipStream_t stream) {
+  const int d = a.d;
+#define DLRM_CALL(L, N) launch_fwd_width<T, TY, VE, L, N>(a, stream)
+  DLRM_NORM_WIDTHS(DLRM_CALL)
+#undef DLRM_CALL
+}
 template <class T, class TY>
-int launch_fwd(const void* x, int64_t x_ld, const void* res, int64_t res_ld, const float* w, int64_t n, int d,
-               float eps, uint32_t cut, const int64_t* rng, void* h, int64_t h_ld, void* y, int64_t y_ld,
-               float* scale_bias, float* rstd, hipStream_t stream) {
-  hipLaunchKernelGGL((addnorm_fwd_kernel<T, TY>), dim3((unsigned)(n < 65536 ? n : 65536)), dim3(kThreads), 0, stream,
-                     static_cast<const T*>(x), x_ld, static_cast<const T*>(res), res_ld, w, n, d, eps, cut,
-                     drop_factor(cut), rng, static_cast<T*>(h), h_ld, static_cast<TY*>(y), y_ld, scale_bias, rstd);
+int launch_fwd(const Fwd& a, hipStream_t stream) {
+  auto fits = [&](int ve) {
+    auto ok = [&](const void* p, int64_t ld, size_t e) { return !p || rows_aligned(p, ld, e, ve * e < 16 ? ve * e : 16); };
+    return a.d % ve == 0 && ok(a.x, a.x_ld, sizeof(T)) && ok(a.res, a.res_ld, sizeof(T)) &&
+           ok(a.h, a.h_ld, sizeof(T)) && ok(a.y, a.y_ld, sizeof(TY)) && aligned16(a.w) &&
+           (reinterpret_cast<uintptr_t>(a.scale_bias) & 7u) == 0;
+  };
+  if (fits(8)) return launch_fwd_pieces<T, TY, 8>(a, stream);
+  if (fits(4)) return launch_fwd_pieces<T, TY, 4>(a, stream);
+  hipLaunchKernelGGL((addnorm_fwd_odd_kernel<T, TY>), dim3((unsigned)(a.n < 65536 ? a.n : 65536)), dim3(kThreads),
+                     4 * (unsigned)a.d, stream, a);
   return launch_status();
 }
 
+template <class T, int VE, int LPR, int NP>
+int launch_bwd_width(const Bwd& a, int blocks, hipStream_t stream) {
+  hipLaunchKernelGGL((addnorm_bwd_kernel<T, VE, LPR, NP>), dim3(blocks), dim3(kThreads), 0, stream, a);
+  return launch_status();
+}
+template <class T, int VE>
+int launch_bwd_pieces(const Bwd& a, int blocks, hipStream_t stream) {
+  const int d = a.d;
+#define DLRM_CALL(L, N) launch_bwd_width<T, VE, L, N>(a, blocks, stream)
+  DLRM_NORM_WIDTHS(DLRM_CALL)
+#undef DLRM_CALL
+}
 template <class T>
-int launch_bwd(const void* dy, int64_t dy_ld, const void* dh, int64_t dh_ld, const void* h, int64_t h_ld,
-               const float* w, const float* rstd, int64_t n, int d, uint32_t cut, const int64_t* rng, void* dx,
-               int64_t dx_ld, void* dres, int64_t dres_ld, float* dw, float* part, hipStream_t stream) {
-  const int blocks = (int)(n < kBwdBlocks ? n : kBwdBlocks);
-  if (blocks > 0)
-    hipLaunchKernelGGL((addnorm_bwd_kernel<T>), dim3(blocks), dim3(kThreads), 0, stream, static_cast<const T*>(dy),
-                       dy_ld, static_cast<const T*>(dh), dh_ld, static_cast<const T*>(h), h_ld, w, rstd, n, d, cut,
-                       drop_factor(cut), rng, static_cast<T*>(dx), dx_ld, static_cast<T*>(dres), dres_ld, part);
-  hipLaunchKernelGGL(dw_kernel, dim3((unsigned)ceil_div(d, kThreads)), dim3(kThreads), 0, stream, part, blocks, d, dw);
+int launch_bwd(const Bwd& a, float* dw, hipStream_t stream) {
+  auto fits = [&](int ve) {
+    auto ok = [&](const void* p, int64_t ld) {
+      return !p || rows_aligned(p, ld, sizeof(T), ve * sizeof(T) < 16 ? ve * sizeof(T) : 16);
+    };
+    return a.d % ve == 0 && ok(a.dy, a.dy_ld) && ok(a.dh, a.dh_ld) && ok(a.h, a.h_ld) && ok(a.dx, a.dx_ld) &&
+           ok(a.dres, a.dres_ld) && aligned16(a.w);
+  };
+  const int blocks = (int)(a.n < kBwdBlocks ? a.n : kBwdBlocks);
+  int rc = DLRM_OK;
+  if (blocks == 0) {
+  } else if (fits(8)) {
+    rc = launch_bwd_pieces<T, 8>(a, blocks, stream);
+  } else if (fits(4)) {
+    rc = launch_bwd_pieces<T, 4>(a, blocks, stream);
+  } else {
+    hipLaunchKernelGGL((addnorm_bwd_odd_kernel<T>), dim3(blocks), dim3(kThreads), 4 * (unsigned)a.d, stream, a);
+    rc = launch_status();
+  }
+  if (rc != DLRM_OK) return rc;
+  hipLaunchKernelGGL(dw_kernel, dim3((unsigned)ceil_div(a.d, kDwCols)), dim3(kThreads), 0, stream, a.part, blocks, a.d,
+                     dw);
   return launch_status();
 }
 
@@ -181,18 +507,9 @@ extern "C" int dlrm_add_rmsnorm_fwd(const void* x, int64_t x_ld, const void* res
   if ((h && h == x && h_ld != x_ld) || (h && h == res && h_ld != res_ld)) return DLRM_E_INVALID;
   if (n > (1LL << 40) / d) return DLRM_E_UNSUPPORTED;
   const uint32_t cut = drop_cut(p);
-  if (dtype == DLRM_F32) {
-    if (i8)
-      return launch_fwd<float, int8_t>(x, x_ld, res, res_ld, w, n, d, eps, cut, rng, h, h_ld, y, y_ld, scale_bias,
-                                       rstd, stream);
-    return launch_fwd<float, float>(x, x_ld, res, res_ld, w, n, d, eps, cut, rng, h, h_ld, y, y_ld, nullptr, rstd,
-                                    stream);
-  }
-  if (i8)
-    return launch_fwd<uint16_t, int8_t>(x, x_ld, res, res_ld, w, n, d, eps, cut, rng, h, h_ld, y, y_ld, scale_bias,
-                                        rstd, stream);
-  return launch_fwd<uint16_t, uint16_t>(x, x_ld, res, res_ld, w, n, d, eps, cut, rng, h, h_ld, y, y_ld, nullptr, rstd,
-                                        stream);
+  const Fwd a{x, res, x_ld, res_ld, w, n, d, eps, cut, drop_factor(cut), rng, h, y, h_ld, y_ld, scale_bias, rstd};
+  if (dtype == DLRM_F32) return i8 ? launch_fwd<float, int8_t>(a, stream) : launch_fwd<float, float>(a, stream);
+  return i8 ? launch_fwd<uint16_t, int8_t>(a, stream) : launch_fwd<uint16_t, uint16_t>(a, stream);
 }
 
 extern "C" size_t dlrm_add_rmsnorm_bwd_workspace_size(int64_t n, int32_t d) {
@@ -218,11 +535,8 @@ extern "C" int dlrm_add_rmsnorm_bwd(const void* dy, int64_t dy_ld, const void* d
   if (n > (1LL << 40) / d) return DLRM_E_UNSUPPORTED;
   if (n > 0 && (!ws || ws_bytes < dlrm_add_rmsnorm_bwd_workspace_size(n, d))) return DLRM_E_WORKSPACE;
   if (reinterpret_cast<uintptr_t>(ws) & 255u) return DLRM_E_INVALID;
-  float* part = static_cast<float*>(ws);
   const uint32_t cut = drop_cut(p);
-  if (dtype == DLRM_F32)
-    return launch_bwd<float>(dy, dy_ld, dh, dh_ld, h, h_ld, w, rstd, n, d, cut, rng, dx, dx_ld, dres, dres_ld, dw,
-                             part, stream);
-  return launch_bwd<uint16_t>(dy, dy_ld, dh, dh_ld, h, h_ld, w, rstd, n, d, cut, rng, dx, dx_ld, dres, dres_ld, dw,
-                              part, stream);
+  const Bwd a{dy, dh, h, dy_ld, dh_ld, h_ld, w, rstd, n, d, cut, drop_factor(cut), rng, dx, dres, dx_ld, dres_ld,
+              static_cast<float*>(ws)};
+  return dtype == DLRM_F32 ? launch_bwd<float>(a, dw, stream) : launch_bwd<uint16_t>(a, dw, stream);
 }
