@@ -534,10 +534,13 @@ __global__ __launch_bounds__(kThreads) void linattn_kernel(Plan plan) {
 }
 
 // The states that enter the segments, in place of those that the segments
-// made from zero: in[s] = decay^seg_len in[s - 1] + made[s - 1].
+// made from zero: in[s] = decay^seg_len in[s - 1] + made[s - 1].  A thread
+// takes four elements along the segments, kAhead loads in flight.
+constexpr int kAhead = 16;
 template <class T, int DK, int VS>
 __global__ __launch_bounds__(kThreads) void linattn_scan_kernel(Plan plan) {
   using Sh = Shape<T, DK, VS>;
+  using St = State<T, DK, VS>;
   constexpr int64_t kBlobFloats = (int64_t)Sh::kBlob * kThreads;
   int64_t bh;
   int in;
@@ -546,48 +549,113 @@ __global__ __launch_bounds__(kThreads) void linattn_scan_kernel(Plan plan) {
   const int h = (int)(bh - b * plan.H);
   const Role& role = plan.roles.r[in / plan.slices];
   const int64_t len = plan.offsets[b + 1] - plan.offsets[b];
+  const int used = len > 0 ? (int)((len + plan.seg_len - 1) / plan.seg_len) : 1;  // segments that have rows
   const float l2 = log2f(plan.decay[h]);
   const float all = exp2f(l2 * (float)plan.seg_len);
-  State<T, DK, VS> S, made;
-  if (role.first) S.load(role.first + bh * role.dk * role.dv, role.flip, in % plan.slices * VS, role.dk, role.dv);
-  else S.clear();
-  for (int seg = 0; seg < plan.segments && (seg == 0 || seg * plan.seg_len < len); ++seg) {
-    float* p = plan.blobs + ((bh * plan.segments + seg) * plan.inner + in) * kBlobFloats;
-    const bool more = (seg + 1) * plan.seg_len < len;
-    if (more) made.load_blob(p);
-    S.store_blob(p);
-    if (!more) break;
+  const int i = blockIdx.y / Sh::kNW, j = blockIdx.y % Sh::kNW;
+  f32x4 s{0.f, 0.f, 0.f, 0.f};
+  if (role.first) {
+    const int r = St::row(i), c = in % plan.slices * VS + Sh::column(threadIdx.x & 15, St::tile(j));
+    const float* p = role.first + bh * role.dk * role.dv;
+    if (r < role.dk && c < role.dv) {
+      if (role.flip) s = *reinterpret_cast<const f32x4*>(p + (int64_t)c * role.dk + r);
+      else
 #pragma unroll
-    for (int i = 0; i < Sh::kMW; ++i)
+        for (int e = 0; e < 4; ++e) s[e] = p[(r + e) * role.dv + c];
+    }
+  }
+  const int64_t pitch = plan.inner * kBlobFloats / 4;
+  f32x4* p = reinterpret_cast<f32x4*>(plan.blobs + (bh * plan.segments * plan.inner + in) * kBlobFloats) +
+             (int64_t)blockIdx.y * kThreads + threadIdx.x;
+  for (int s0 = 0; s0 < used; s0 += kAhead) {
+    f32x4 made[kAhead];
 #pragma unroll
-      for (int j = 0; j < Sh::kNW; ++j)
+    for (int u = 0; u < kAhead; ++u)
+      if (s0 + u + 1 < used) made[u] = p[(s0 + u) * pitch];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) S.t[i][j][r] = S.t[i][j][r] * all + made.t[i][j][r];
+    for (int u = 0; u < kAhead; ++u) {
+      if (s0 + u >= used) break;
+      p[(s0 + u) * pitch] = s;
+      if (s0 + u + 1 < used) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] = s[e] * all + made[u][e];
+      }
+    }
   }
 }
 
-template <class T>
-__global__ __launch_bounds__(128) void linattn_step_kernel(Strided q, Strided k, Strided v, Strided o, int H, int dk,
-                                                           int dv, const float* __restrict__ decay, float scale,
-                                                           float* __restrict__ state,
-                                                           const int64_t* __restrict__ slots) {
+// One new event for one user and head: the state is read and written once,
+// 16 bytes per lane and kInFlight rows of a lane's columns at a time; LPR
+// lanes cover a row's dv columns, the block's other lanes other rows, and
+// their parts of o are added in a fixed order (lanes of a wave, then waves).
+constexpr int kInFlight = 4;
+template <class T, int LPR>
+__global__ __launch_bounds__(kThreads) void linattn_step_kernel(Strided q, Strided k, Strided v, Strided o, int H, int dk,
+                                                                int dv, const float* __restrict__ decay, float scale,
+                                                                float* __restrict__ state,
+                                                                const int64_t* __restrict__ slots) {
+  constexpr int RPB = kThreads / LPR;  // rows side by side
+  __shared__ f32x4 part[kThreads / 64][LPR];
   const int64_t b = blockIdx.x / H;
-  const int h = blockIdx.x - (int)b * H, j = threadIdx.x;
-  if (j >= dv) return;
+  const int h = blockIdx.x - (int)b * H;
   const int64_t slot = slots ? slots[b] : b;
-  float acc = 0.f;
-  if (slot >= 0) {
-    float* S = state + (slot * H + h) * dk * dv;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int c = (threadIdx.x & (LPR - 1)) * 4, r0 = threadIdx.x / LPR;
+  f32x4 acc{0.f, 0.f, 0.f, 0.f};
+  if (slot >= 0 && c < dv) {
+    float* S = state + (slot * H + h) * dk * dv + c;
     const T* qp = static_cast<const T*>(q.p) + b * q.ts + h * q.hs;
     const T* kp = static_cast<const T*>(k.p) + b * k.ts + h * k.hs;
-    const float vj = to_f32(static_cast<const T*>(v.p)[b * v.ts + h * v.hs + j]), lam = decay[h];
-    for (int i = 0; i < dk; ++i) {
-      const float u = lam * S[i * dv + j] + to_f32(kp[i]) * vj;
-      S[i * dv + j] = u;
-      acc += to_f32(qp[i]) * u;
+    f32x4 vv;
+    {
+      Piece<T, 4> p;
+      p.load(static_cast<const T*>(v.p) + b * v.ts + h * v.hs + c);
+      float x[4];
+      p.get(x);
+      vv = f32x4{x[0], x[1], x[2], x[3]};
+    }
+    const float lam = decay[h];
+    for (int r = r0; r < dk; r += RPB * kInFlight) {
+      f32x4 s[kInFlight];
+      float qv[kInFlight], kv[kInFlight];
+#pragma unroll
+      for (int u = 0; u < kInFlight; ++u) {
+        const int row = r + u * RPB;
+        if (row < dk) {
+          s[u] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(S + row * dv));
+          qv[u] = to_f32(qp[row]);
+          kv[u] = to_f32(kp[row]);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kInFlight; ++u) {
+        const int row = r + u * RPB;
+        if (row < dk) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            s[u][e] = __builtin_fmaf(lam, s[u][e], kv[u] * vv[e]);
+            acc[e] = __builtin_fmaf(qv[u], s[u][e], acc[e]);
+          }
+          __builtin_nontemporal_store(s[u], reinterpret_cast<f32x4*>(S + row * dv));
+        }
+      }
     }
   }
-  static_cast<T*>(const_cast<void*>(o.p))[b * o.ts + h * o.hs + j] = from_f32<T>(acc * scale);
+#pragma unroll
+  for (int off = LPR; off < 64; off <<= 1)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] += __shfl_xor(acc[e], off, 64);
+  if (lane < LPR) part[wave][lane] = acc;
+  __syncthreads();
+  if (threadIdx.x < LPR && c < dv) {
+    f32x4 t = part[0][threadIdx.x];
+#pragma unroll
+    for (int w = 1; w < kThreads / 64; ++w) t += part[w][threadIdx.x];
+    const float x[4] = {t[0] * scale, t[1] * scale, t[2] * scale, t[3] * scale};
+    Piece<T, 4> p;
+    p.set(x);
+    p.store(static_cast<T*>(const_cast<void*>(o.p)) + b * o.ts + h * o.hs + c);
+  }
 }
 
 bool head_ok(int32_t w) { return w >= 8 && w <= 128 && w % 8 == 0; }
@@ -663,7 +731,9 @@ int launch_shape(const Plan& plan, hipStream_t stream) {
   if (plan.segments > 1) {
     hipLaunchKernelGGL((linattn_kernel<T, DK, VS, true>), blocks(plan.units * (plan.segments - 1)), dim3(kThreads), lds,
                        stream, plan);
-    hipLaunchKernelGGL((linattn_scan_kernel<T, DK, VS>), blocks(plan.units), dim3(kThreads), 0, stream, plan);
+    dim3 scan = blocks(plan.units);
+    scan.y = Shape<T, DK, VS>::kBlob / 4;
+    hipLaunchKernelGGL((linattn_scan_kernel<T, DK, VS>), scan, dim3(kThreads), 0, stream, plan);
   }
   hipLaunchKernelGGL((linattn_kernel<T, DK, VS, false>), blocks(plan.units * plan.segments), dim3(kThreads), lds, stream,
                      plan);
@@ -697,6 +767,21 @@ int launch(const Role* roles, int count, int32_t dtype, const int64_t* offsets, 
   cut(p.units * p.inner, max_len, &p.segments, &p.seg_len);
   for (int i = 0; i < count; ++i) p.roles.r[i] = roles[i];
   return dtype == DLRM_F32 ? launch_type<float>(p, stream) : launch_type<uint16_t>(p, stream);
+}
+
+template <class T>
+int launch_step(const Strided& q, const Strided& k, const Strided& v, const Strided& o, int64_t B, int32_t H, int32_t dk,
+                int32_t dv, const float* decay, float scale, float* state, const int64_t* slots, hipStream_t stream) {
+  const dim3 grid((unsigned)(B * H)), block(kThreads);
+#define DLRM_STEP(L)                                                                                                  \
+  hipLaunchKernelGGL((linattn_step_kernel<T, L>), grid, block, 0, stream, q, k, v, o, H, dk, dv, decay, scale, state, \
+                     slots)
+  if (dv <= 16) DLRM_STEP(4);
+  else if (dv <= 32) DLRM_STEP(8);
+  else if (dv <= 64) DLRM_STEP(16);
+  else DLRM_STEP(32);
+#undef DLRM_STEP
+  return launch_status();
 }
 
 // Whether the backward pass's three roles fit one launch: equal padded widths
@@ -778,12 +863,6 @@ extern "C" int dlrm_linattn_step(const void* q, int64_t q_bs, int64_t q_hs, cons
   if (!strided_ok(Q) || !strided_ok(K) || !strided_ok(V) || !strided_ok(O) || !decay || !state || !state_ok(state))
     return DLRM_E_INVALID;
   if (B > 0x7fffffffLL / 32 / H) return DLRM_E_UNSUPPORTED;
-  const dim3 grid((unsigned)(B * H));
-  if (dtype == DLRM_F32)
-    hipLaunchKernelGGL((linattn_step_kernel<float>), grid, dim3(128), 0, stream, Q, K, V, O, H, dk, dv, decay, scale,
-                       state, slots);
-  else
-    hipLaunchKernelGGL((linattn_step_kernel<uint16_t>), grid, dim3(128), 0, stream, Q, K, V, O, H, dk, dv, decay,
-                       scale, state, slots);
-  return launch_status();
+  return dtype == DLRM_F32 ? launch_step<float>(Q, K, V, O, B, H, dk, dv, decay, scale, state, slots, stream)
+                           : launch_step<uint16_t>(Q, K, V, O, B, H, dk, dv, decay, scale, state, slots, stream);
 }

@@ -261,19 +261,21 @@ int bits_for(int64_t x) {  // bits needed to hold 0..x
   return b;
 }
 
-// Digits of 8 bits, or 9 where that saves a pass (26 key bits: three passes
-// of 9 instead of four of 8).
+// Digits of 8 bits, or wider ones (up to max_digit_bits) where that saves a
+// pass (26 key bits: three passes of 9 instead of four of 8).
 struct SortPlan {
   int passes, digit_bits;
 };
-SortPlan sort_plan(int row_bits) {
-  const int p8 = (row_bits + 7) / 8, p9 = (row_bits + 8) / 9;
-  return p9 < p8 ? SortPlan{p9, 9} : SortPlan{p8, 8};
+SortPlan sort_plan(int key_bits, int max_digit_bits) {
+  SortPlan p{(key_bits + 7) / 8, 8};
+  for (int b = 9; b <= max_digit_bits; ++b)
+    if ((key_bits + b - 1) / b < p.passes) p = SortPlan{(key_bits + b - 1) / b, b};
+  return p;
 }
 
 // Every pass of the plan over keys[0] / vals[0]; the sorted pairs end in
-// buffer passes % 2, which is returned.  counts and offsets hold tiles << 9
-// words, sums one row of 1 << 9 per kChunk tiles.
+// buffer passes % 2, which is returned.  counts and offsets hold tiles
+// rows of 1 << digit_bits words, sums one such row per kChunk tiles.
 int launch_sort(const SortPlan& plan, uint32_t* const (&keys)[2], int32_t* const (&vals)[2], uint32_t* counts,
                 uint32_t* sums, uint32_t* offsets, int n, hipStream_t stream) {
   const unsigned tiles = (unsigned)ceil_div(n, TILE);
@@ -288,7 +290,9 @@ int launch_sort(const SortPlan& plan, uint32_t* const (&keys)[2], int32_t* const
   hipLaunchKernelGGL(tile_offset_kernel<DB>, chunk_grid, dim3(RT), 0, stream, counts, sums, (int)tiles, offsets);  \
   hipLaunchKernelGGL(scatter_kernel<DB>, dim3(tiles), dim3(RT), 0, stream, keys[cur], vals[cur], keys[cur ^ 1],    \
                      vals[cur ^ 1], n, shift, offsets, (int)tiles)
-    if (plan.digit_bits == 9) {
+    if (plan.digit_bits == 10) {
+      DLRM_PASS(10);
+    } else if (plan.digit_bits == 9) {
       DLRM_PASS(9);
     } else {
       DLRM_PASS(8);

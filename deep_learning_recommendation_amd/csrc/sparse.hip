@@ -759,7 +759,7 @@ extern "C" int dlrm_embbag_bwd_sgd_prepare(int32_t K, const int64_t* rows, const
   // the sort runs over the row bits only: positions are table-major (the
   // bags of table k come before those of table k + 1), so a stable sort by
   // row leaves equal rows in table order and every (table, row) key in one run
-  const SortPlan plan = sort_plan(row_bits);
+  const SortPlan plan = sort_plan(row_bits, 9);
   const unsigned tiles = (unsigned)L.tiles;
   const int cur = launch_sort(plan, b.keys, b.vals, b.counts, b.sums, b.offsets, n, stream);
   hipLaunchKernelGGL(heads_count_kernel, dim3(tiles), dim3(RT), 0, stream, b.keys[cur], n, b.counts);
@@ -786,7 +786,7 @@ extern "C" int dlrm_embbag_bwd_sgd_apply(float* const* tables, int32_t K, int32_
   SparseLayout L;
   SparseBufs b;
   if ((rc = sparse_bufs(nnz, d, ws, ws_bytes, &L, &b)) != DLRM_OK) return rc;
-  const int cur = sort_plan(row_bits).passes & 1;
+  const int cur = sort_plan(row_bits, 9).passes & 1;
   // the short segments' work counter starts from zero on every call, so one
   // prepared workspace can be applied more than once; it is cleared on the
   // stream whose kernel takes work from it

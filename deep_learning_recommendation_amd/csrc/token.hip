@@ -10,9 +10,9 @@
 //
 // Gradient.  The positions are sorted by token (radix_sort.hpp: stable, so a
 // row's positions stay in order), which turns the scattered sums into runs.
-// The sorted list is cut into chunks of kChunkLen positions whatever the runs
-// are, one lane group per chunk: the load is even for uniform tokens and for
-// a popular token with 1e5 occurrences alike, without a list of runs.  A run
+// The sorted list is cut into chunks of equal length whatever the runs are,
+// one lane group per chunk: the load is even for uniform tokens and for a
+// popular token with 1e5 occurrences alike, without a list of runs.  A run
 // inside a chunk goes straight to its table row; a run that crosses chunk
 // ends leaves one partial sum per chunk (head: it began earlier; tail: it
 // begins here and goes on), and a second kernel adds a run's partials in a
@@ -83,7 +83,17 @@ int launch_fwd(const void* table, int64_t rows, int d, const int64_t* tokens, in
 
 // ------------------------------------------------------------------ gradient
 
-constexpr int kChunkLen = 64;  // sorted positions per chunk
+// Sorted positions per chunk: long chunks leave few partial sums, short ones
+// give enough lane groups when there are few positions.
+constexpr int kLongChunk = 64, kShortChunk = 16;
+int chunk_len(int64_t n) { return n >= 65536 ? kLongChunk : kShortChunk; }
+
+__device__ __forceinline__ uint32_t token_key(int64_t t, int64_t rows) {
+  return (uint32_t)(t >= 0 && t < rows ? t : rows);
+}
+__device__ __forceinline__ void zero_rows(float4* zero, int64_t zero4, int64_t at, int64_t step) {
+  for (int64_t i = at; i < zero4; i += step) zero[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+}
 
 // Keys (the token, or `rows` for one that names no row: those sort last) and
 // positions; and, unless the gradient is added to what the table gradient
@@ -93,11 +103,106 @@ __global__ __launch_bounds__(256) void token_keys_kernel(const int64_t* __restri
                                                          float4* __restrict__ zero, int64_t zero4) {
   const int64_t at = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, step = (int64_t)gridDim.x * blockDim.x;
   for (int64_t i = at; i < n; i += step) {
-    const int64_t t = tokens[i];
-    keys[i] = (uint32_t)(t >= 0 && t < rows ? t : rows);
+    keys[i] = token_key(tokens[i], rows);
     vals[i] = (int32_t)i;
   }
-  for (int64_t i = at; i < zero4; i += step) zero[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  zero_rows(zero, zero4, at, step);
+}
+
+// Few tokens: block 0 does the whole sort in LDS (the ranking of
+// scatter_kernel, digit by digit) while the others clear the table gradient.
+// One launch instead of the nine of two global passes, whose time would all
+// be launches.
+constexpr int kSmallThreads = 1024, kSmallItems = 8, kSmallMax = kSmallThreads * kSmallItems;
+__global__ __launch_bounds__(kSmallThreads) void token_sort_small_kernel(const int64_t* __restrict__ tokens, int n,
+                                                                         int64_t rows, int key_bits,
+                                                                         uint32_t* __restrict__ keys,
+                                                                         int32_t* __restrict__ vals,
+                                                                         float4* __restrict__ zero, int64_t zero4) {
+  constexpr int NB = 256, W = kSmallThreads / 64;
+  __shared__ uint32_t lk[kSmallMax];
+  __shared__ int32_t lv[kSmallMax];
+  __shared__ uint32_t cnt[W][NB];
+  __shared__ uint32_t tot[NB / 64];
+  if (blockIdx.x > 0) {  // there when zero4 > 0
+    zero_rows(zero, zero4, (int64_t)(blockIdx.x - 1) * kSmallThreads + threadIdx.x,
+              (int64_t)(gridDim.x - 1) * kSmallThreads);
+    return;
+  }
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const uint64_t below = (lane == 0) ? 0ull : (~0ull >> (64 - lane));
+  const int items = (n + kSmallThreads - 1) / kSmallThreads;  // wave w holds positions (w items + i) 64 + lane
+  auto pos = [&](int i) { return (wave * items + i) * 64 + lane; };
+  for (int i = 0; i < items; ++i)
+    if (pos(i) < n) {
+      lk[pos(i)] = token_key(tokens[pos(i)], rows);
+      lv[pos(i)] = pos(i);
+    }
+  for (int shift = 0; shift < key_bits; shift += 8) {
+    for (int i = tid; i < W * NB; i += kSmallThreads) (&cnt[0][0])[i] = 0u;
+    __syncthreads();
+    uint32_t key[kSmallItems], rank[kSmallItems];
+    int32_t val[kSmallItems];
+#pragma unroll
+    for (int i = 0; i < kSmallItems; ++i) {
+      if (i >= items) break;
+      const bool valid = pos(i) < n;
+      key[i] = valid ? lk[pos(i)] : 0u;
+      val[i] = valid ? lv[pos(i)] : 0;
+      const uint32_t dg = (key[i] >> shift) & (NB - 1);
+      uint64_t peers = __ballot(valid);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const bool bit = (dg >> q) & 1u;
+        const uint64_t m = __ballot(bit);
+        peers &= bit ? m : ~m;
+      }
+      const uint32_t before = valid ? cnt[wave][dg] : 0u;
+      rank[i] = before + (uint32_t)__popcll(peers & below);
+      if (valid && (peers & below) == 0ull) cnt[wave][dg] = before + (uint32_t)__popcll(peers);
+    }
+    __syncthreads();
+    // a digit's start, then each wave's within it
+    uint32_t run = 0, incl = 0;
+    if (tid < NB) {
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const uint32_t c = cnt[w][tid];
+        cnt[w][tid] = run;
+        run += c;
+      }
+      incl = run;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const uint32_t y = __shfl_up(incl, o, 64);
+        if (lane >= o) incl += y;
+      }
+      if (lane == 63) tot[wave] = incl;
+    }
+    __syncthreads();
+    if (tid < NB) {
+      uint32_t start = incl - run;
+      for (int w = 0; w < wave; ++w) start += tot[w];
+#pragma unroll
+      for (int w = 0; w < W; ++w) cnt[w][tid] += start;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kSmallItems; ++i) {
+      if (i >= items) break;
+      if (pos(i) < n) {
+        const uint32_t to = cnt[wave][(key[i] >> shift) & (NB - 1)] + rank[i];
+        lk[to] = key[i];
+        lv[to] = val[i];
+      }
+    }
+    __syncthreads();
+  }
+  for (int i = 0; i < items; ++i)
+    if (pos(i) < n) {
+      keys[pos(i)] = lk[pos(i)];
+      vals[pos(i)] = lv[pos(i)];
+    }
 }
 
 template <int VE>
@@ -120,23 +225,37 @@ __device__ __forceinline__ void put_part(float* p, const float (&acc)[VE]) {
     *reinterpret_cast<float4*>(p + c) = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
 }
 
-// One lane group per chunk and column slice (blockIdx.y).
+// One lane group per chunk and column slice (blockIdx.y).  The block's keys
+// and positions come through LDS; 2 U rows are in flight per group.
 template <class T, int VE, int U>
 __global__ __launch_bounds__(256) void token_chunk_kernel(const uint32_t* __restrict__ keys,
                                                           const int32_t* __restrict__ vals, int n, uint32_t rows,
-                                                          const T* __restrict__ dout, int64_t ld, int d, int g_log2,
-                                                          float scale, bool add, float* __restrict__ dtable,
-                                                          float* __restrict__ head, float* __restrict__ tail) {
+                                                          int chunk_len, const T* __restrict__ dout, int64_t ld, int d,
+                                                          int g_log2, float scale, bool add,
+                                                          float* __restrict__ dtable, float* __restrict__ head,
+                                                          float* __restrict__ tail) {
+  extern __shared__ uint32_t staged[];  // keys, then positions, of the block's chunks
   const int GL = 1 << g_log2, gl = threadIdx.x & (GL - 1);
-  const int64_t chunk = (int64_t)blockIdx.x * (256 >> g_log2) + (threadIdx.x >> g_log2);
-  const int64_t c0 = chunk * kChunkLen;
-  if (c0 >= n) return;  // whole group
-  const int len = (int)(n - c0 < kChunkLen ? n - c0 : kChunkLen);
+  const int span = (256 >> g_log2) * chunk_len;
+  const int64_t b0 = (int64_t)blockIdx.x * span;
+  for (int i = threadIdx.x; i < span; i += 256) {
+    const bool in = b0 + i < n;
+    staged[i] = in ? keys[b0 + i] : rows;
+    staged[span + i] = in ? (uint32_t)vals[b0 + i] : 0u;
+  }
+  const int grp = threadIdx.x >> g_log2;
+  const int64_t chunk = (int64_t)blockIdx.x * (256 >> g_log2) + grp, c0 = chunk * chunk_len;
+  // the keys on either side (no key is ~0)
+  const uint32_t before = c0 > 0 && c0 < n ? keys[c0 - 1] : ~0u;
+  const uint32_t after = c0 + chunk_len < n ? keys[c0 + chunk_len] : ~0u;
+  __syncthreads();
+  const uint32_t* ck = staged + grp * chunk_len;
+  const uint32_t* cp = ck + span;
+  uint32_t cur = ck[0];
+  if (cur >= rows) return;  // padding, or past the end
+  bool open = before == cur;  // the run began before this chunk
   const int col = ((int)blockIdx.y * GL + gl) * VE;
   const bool on = col < d;
-  uint32_t cur = keys[c0];
-  if (cur >= rows) return;  // padding only
-  bool open = c0 > 0 && keys[c0 - 1] == cur;  // the run began before this chunk
   float acc[VE];
 #pragma unroll
   for (int c = 0; c < VE; ++c) acc[c] = 0.f;
@@ -145,89 +264,147 @@ __global__ __launch_bounds__(256) void token_chunk_kernel(const uint32_t* __rest
     if (open) put_part<VE>(head + chunk * d + col, acc);
     else put_row<VE>(dtable + (int64_t)cur * d + col, acc, scale, add);
   };
-  for (int q0 = 0; q0 < len; q0 += GL) {
-    const int m = min(GL, len - q0);
-    const uint32_t my_key = gl < m ? keys[c0 + q0 + gl] : rows;
-    const int32_t my_pos = gl < m ? vals[c0 + q0 + gl] : 0;
-    for (int u0 = 0; u0 < m; u0 += U) {
-      Piece<T, VE> in[U];
-      uint32_t key[U];
+  Piece<T, VE> in[2][U];
+  auto fetch = [&](int q0, Piece<T, VE> (&to)[U]) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int src = u0 + u < m ? u0 + u : m - 1;
-        key[u] = (uint32_t)__shfl((int)my_key, src, GL);
-        const int64_t pos = __shfl(my_pos, src, GL);
-        if (u0 + u >= m) key[u] = rows;
-        if (on && key[u] < rows) in[u].load(dout + pos * ld + col);
+    for (int u = 0; u < U; ++u)
+      if (on && q0 + u < chunk_len && ck[q0 + u] < rows) to[u].load(dout + (int64_t)cp[q0 + u] * ld + col);
+  };
+  auto take = [&](int q0, const Piece<T, VE> (&from)[U]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t key = q0 + u < chunk_len ? ck[q0 + u] : rows;
+      if (key >= rows) continue;
+      if (key != cur) {
+        close();
+        cur = key;
+        open = false;
+#pragma unroll
+        for (int c = 0; c < VE; ++c) acc[c] = 0.f;
       }
+      if (on) {
+        float v[VE];
+        from[u].get(v);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (key[u] >= rows) continue;
-        if (key[u] != cur) {
-          close();
-          cur = key[u];
-          open = false;
-#pragma unroll
-          for (int c = 0; c < VE; ++c) acc[c] = 0.f;
-        }
-        if (on) {
-          float v[VE];
-          in[u].get(v);
-#pragma unroll
-          for (int c = 0; c < VE; ++c) acc[c] += v[c];
-        }
+        for (int c = 0; c < VE; ++c) acc[c] += v[c];
       }
     }
+  };
+  fetch(0, in[0]);
+  for (int q0 = 0; q0 < chunk_len; q0 += 2 * U) {
+    fetch(q0 + U, in[1]);
+    take(q0, in[0]);
+    fetch(q0 + 2 * U, in[0]);
+    take(q0 + U, in[1]);
   }
-  const bool goes_on = c0 + len < n && keys[c0 + len] == cur;
-  if (!goes_on) close();
+  if (after != cur) close();
   else if (on) put_part<VE>((open ? head : tail) + chunk * d + col, acc);
 }
 
 // One wave per chunk whose last run begins in it and goes on: tail of this
 // chunk plus the heads of the chunks that the run reaches, the wave's lane
-// groups taking every groups-th partial, then added across groups.
+// groups taking every groups-th partial, then added across groups.  Runs of
+// more than kJoinWave partials (a popular token's) are taken by the whole
+// block, one after the other.
+constexpr int kJoinThreads = 1024, kJoinWaves = kJoinThreads / 64, kJoinWave = 64, kJoinFlight = 8;
+
+// partials first, first + step, ... up to m of the run that begins in `chunk`
 template <int VE>
-__global__ __launch_bounds__(256) void token_join_kernel(const uint32_t* __restrict__ keys, int n, uint32_t rows, int d,
-                                                         int g_log2, float scale, bool add,
-                                                         float* __restrict__ dtable, const float* __restrict__ head,
-                                                         const float* __restrict__ tail) {
-  const int lane = threadIdx.x & 63;
-  const int64_t chunk = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int64_t c0 = chunk * kChunkLen, c1 = c0 + kChunkLen;
-  if (c1 >= n) return;
-  const uint32_t key = keys[c1 - 1];
-  if (key >= rows || keys[c1] != key) return;
-  if (keys[c0] == key && c0 > 0 && keys[c0 - 1] == key) return;  // began earlier
-  int64_t m = 0;  // chunks after this one that the run reaches
-  for (;;) {
-    const int64_t p = (chunk + 1 + m + lane) * kChunkLen;
-    const uint64_t miss = __ballot(!(p < n && keys[p] == key));
-    if (miss) {
-      m += __ffsll((long long)miss) - 1;
-      break;
+__device__ __forceinline__ void add_partials(const float* __restrict__ head, const float* __restrict__ tail,
+                                             int64_t chunk, int64_t m, int64_t first, int64_t step, int d, int col,
+                                             float (&acc)[VE]) {
+  for (int64_t i0 = first; i0 <= m; i0 += step * kJoinFlight) {
+    Piece<float, VE> p[kJoinFlight];
+#pragma unroll
+    for (int u = 0; u < kJoinFlight; ++u) {
+      const int64_t i = i0 + u * step;
+      if (i <= m) p[u].load((i == 0 ? tail + chunk * d : head + (chunk + i) * d) + col);
     }
-    m += 64;
+#pragma unroll
+    for (int u = 0; u < kJoinFlight; ++u) {
+      if (i0 + u * step > m) break;
+      float v[VE];
+      p[u].get(v);
+#pragma unroll
+      for (int c = 0; c < VE; ++c) acc[c] += v[c];
+    }
   }
-  const int GL = 1 << g_log2, gl = lane & (GL - 1), groups = 64 >> g_log2;
+}
+
+template <int VE>
+__global__ __launch_bounds__(kJoinThreads) void token_join_kernel(const uint32_t* __restrict__ keys, int n,
+                                                                  uint32_t rows, int chunk_len, int d, int g_log2,
+                                                                  float scale, bool add, float* __restrict__ dtable,
+                                                                  const float* __restrict__ head,
+                                                                  const float* __restrict__ tail) {
+  __shared__ int64_t long_m[kJoinWaves];
+  __shared__ float sums[kJoinWaves][64 * VE];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int GL = 1 << g_log2, gl = lane & (GL - 1), groups = 64 >> g_log2, grp = lane >> g_log2;
   const int col = ((int)blockIdx.y * GL + gl) * VE;
   const bool on = col < d;
+  auto wave_sum = [&](float (&acc)[VE]) {
+    for (int o = GL; o < 64; o <<= 1) {
+#pragma unroll
+      for (int c = 0; c < VE; ++c) acc[c] += __shfl_xor(acc[c], o, 64);
+    }
+  };
+  const int64_t chunk = (int64_t)blockIdx.x * kJoinWaves + wave;
+  const int64_t c0 = chunk * chunk_len, c1 = c0 + chunk_len;
+  int64_t m = 0;  // chunks after this one that the run reaches
+  uint32_t key = rows;
+  if (c1 < n) {
+    const uint32_t k0 = keys[c0], k1 = keys[c1 - 1], k2 = keys[c1];
+    const uint32_t kb = c0 > 0 ? keys[c0 - 1] : ~0u;
+    if (k1 < rows && k2 == k1 && !(k0 == k1 && kb == k1)) key = k1;
+  }
+  if (key < rows) {
+    for (;;) {
+      const int64_t p = (chunk + 1 + m + lane) * chunk_len;
+      const uint64_t miss = __ballot(!(p < n && keys[p] == key));
+      if (miss) {
+        m += __ffsll((long long)miss) - 1;
+        break;
+      }
+      m += 64;
+    }
+  }
+  if (lane == 0) long_m[wave] = m > kJoinWave ? m : 0;
   float acc[VE];
 #pragma unroll
   for (int c = 0; c < VE; ++c) acc[c] = 0.f;
-  for (int64_t i = lane >> g_log2; i <= m; i += groups) {
-    const float* p = i == 0 ? tail + chunk * d : head + (chunk + i) * d;
-    if (on) {
+  if (m > 0 && m <= kJoinWave) {
+    if (on) add_partials<VE>(head, tail, chunk, m, grp, groups, d, col, acc);
+    wave_sum(acc);
+    if (on && lane < GL) put_row<VE>(dtable + (int64_t)key * d + col, acc, scale, add);
+  }
+  __syncthreads();
+  for (int w = 0; w < kJoinWaves; ++w) {
+    const int64_t lm = long_m[w], lc = (int64_t)blockIdx.x * kJoinWaves + w;
+    if (lm == 0) continue;  // the whole block
 #pragma unroll
-      for (int c = 0; c < VE; ++c) acc[c] += p[col + c];
+    for (int c = 0; c < VE; ++c) acc[c] = 0.f;
+    if (on) add_partials<VE>(head, tail, lc, lm, wave * groups + grp, kJoinWaves * groups, d, col, acc);
+    wave_sum(acc);
+    if (lane < GL) {
+#pragma unroll
+      for (int c = 0; c < VE; ++c) sums[wave][gl * VE + c] = acc[c];
     }
-  }
-  for (int o = GL; o < 64; o <<= 1) {
+    __syncthreads();
+    if (wave == w && on && lane < GL) {
 #pragma unroll
-    for (int c = 0; c < VE; ++c) acc[c] += __shfl_xor(acc[c], o, 64);
+      for (int c = 0; c < VE; ++c) {
+        float v = sums[0][gl * VE + c];
+        for (int q = 1; q < kJoinWaves; ++q) v += sums[q][gl * VE + c];
+        acc[c] = v;
+      }
+      put_row<VE>(dtable + (int64_t)key * d + col, acc, scale, add);
+    }
+    __syncthreads();
   }
-  if (on && lane < GL) put_row<VE>(dtable + (int64_t)key * d + col, acc, scale, add);
 }
+
+constexpr int kMaxDigitBits = 10;  // a vocabulary of 1M rows: two passes
 
 struct TokenLayout {
   size_t keys[2], vals[2], counts, sums, offsets, head, tail, bytes;
@@ -239,12 +416,12 @@ void token_layout(int64_t n, int d, TokenLayout* L) {
     cv.take<char>(bytes);
     return cv.used - bytes;
   };
-  const int64_t m = n > 0 ? n : 1, tiles = ceil_div(m, TILE), chunks = ceil_div(m, kChunkLen);
+  const int64_t m = n > 0 ? n : 1, tiles = ceil_div(m, TILE), chunks = ceil_div(m, chunk_len(m));
   for (int i = 0; i < 2; ++i) L->keys[i] = take(4 * (size_t)m);
   for (int i = 0; i < 2; ++i) L->vals[i] = take(4 * (size_t)m);
-  L->counts = take(4 * (size_t)kMaxDigits * tiles);
-  L->sums = take(4 * (size_t)kMaxDigits * ceil_div(tiles, kChunk));
-  L->offsets = take(4 * (size_t)kMaxDigits * tiles);
+  L->counts = take(4 * (size_t)(1 << kMaxDigitBits) * tiles);
+  L->sums = take(4 * (size_t)(1 << kMaxDigitBits) * ceil_div(tiles, kChunk));
+  L->offsets = take(4 * (size_t)(1 << kMaxDigitBits) * tiles);
   L->head = take(4 * (size_t)chunks * d);
   L->tail = take(4 * (size_t)chunks * d);
   L->bytes = cv.bytes();
@@ -253,15 +430,16 @@ void token_layout(int64_t n, int d, TokenLayout* L) {
 template <class T, int VE>
 int launch_bwd(const uint32_t* keys, const int32_t* vals, int n, uint32_t rows, const void* dout, int64_t ld, int d,
                float scale, bool add, float* dtable, float* head, float* tail, hipStream_t stream) {
-  const int64_t chunks = ceil_div(n, kChunkLen);
-  const int g = group_log2(d / VE);
+  const int len = chunk_len(n);
+  const int64_t chunks = ceil_div(n, len);
+  const int g = group_log2(d / VE) < 2 ? 2 : group_log2(d / VE);  // at most 64 groups' keys in a block's LDS
   const unsigned slices = (unsigned)ceil_div(d / VE, 1 << g);
-  hipLaunchKernelGGL((token_chunk_kernel<T, VE, 8>), dim3((unsigned)ceil_div(chunks, 256 >> g), slices), dim3(256), 0,
-                     stream, keys, vals, n, rows, static_cast<const T*>(dout), ld, d, g, scale, add, dtable, head,
+  hipLaunchKernelGGL((token_chunk_kernel<T, VE, 8>), dim3((unsigned)ceil_div(chunks, 256 >> g), slices), dim3(256),
+                     8u * (256 >> g) * len, stream, keys, vals, n, rows, len, static_cast<const T*>(dout), ld, d, g, scale, add, dtable, head,
                      tail);
   if (chunks > 1)
-    hipLaunchKernelGGL((token_join_kernel<VE>), dim3((unsigned)ceil_div(chunks, 4), slices), dim3(256), 0, stream, keys,
-                       n, rows, d, g, scale, add, dtable, head, tail);
+    hipLaunchKernelGGL((token_join_kernel<VE>), dim3((unsigned)ceil_div(chunks, kJoinWaves), slices), dim3(kJoinThreads), 0,
+                       stream, keys, n, rows, len, d, g, scale, add, dtable, head, tail);
   return launch_status();
 }
 
@@ -322,12 +500,20 @@ extern "C" int dlrm_token_embed_bwd(const int64_t* tokens, int64_t n, const void
   const int64_t zero4 = add ? 0 : rows * d / 4;
   const int64_t most = n > zero4 ? n : zero4;
   if (most == 0) return DLRM_OK;
-  const int64_t blocks = ceil_div(most, 256);
-  hipLaunchKernelGGL(token_keys_kernel, dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256), 0, stream, tokens,
-                     (int)n, rows, keys[0], vals[0], reinterpret_cast<float4*>(dtable), zero4);
-  if (n == 0) return launch_status();
-  const int cur = launch_sort(sort_plan(bits_for(rows)), keys, vals, u32(L.counts), u32(L.sums), u32(L.offsets), (int)n,
-                              stream);
+  float4* zero = reinterpret_cast<float4*>(dtable);
+  int cur = 0;
+  if (n <= kSmallMax) {
+    const int64_t blocks = 1 + ceil_div(zero4, kSmallThreads * 4);
+    hipLaunchKernelGGL(token_sort_small_kernel, dim3((unsigned)(blocks < 1024 ? blocks : 1024)), dim3(kSmallThreads), 0,
+                       stream, tokens, (int)n, rows, bits_for(rows), keys[0], vals[0], zero, zero4);
+    if (n == 0) return launch_status();
+  } else {
+    const int64_t blocks = ceil_div(most, 256);
+    hipLaunchKernelGGL(token_keys_kernel, dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256), 0, stream, tokens,
+                       (int)n, rows, keys[0], vals[0], zero, zero4);
+    cur = launch_sort(sort_plan(bits_for(rows), kMaxDigitBits), keys, vals, u32(L.counts), u32(L.sums), u32(L.offsets),
+                      (int)n, stream);
+  }
   float* head = reinterpret_cast<float*>(w + L.head);
   float* tail = reinterpret_cast<float*>(w + L.tail);
   const uint32_t r = (uint32_t)rows;
