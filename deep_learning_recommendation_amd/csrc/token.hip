@@ -13,10 +13,11 @@
 // The sorted list is cut into chunks of equal length whatever the runs are,
 // one lane group per chunk: the load is even for uniform tokens and for a
 // popular token with 1e5 occurrences alike, without a list of runs.  A run
-// inside a chunk goes straight to its table row; a run that crosses chunk
-// ends leaves one partial sum per chunk (head: it began earlier; tail: it
-// begins here and goes on), and a second kernel adds a run's partials in a
-// fixed order.  Every row is written once, by one group: no atomics.
+// inside a chunk goes straight to its table row.  A run that crosses chunks
+// is added up in LDS within its block; one that crosses blocks leaves a
+// partial sum per block (head: it began earlier; tail: it begins here and
+// goes on), and a second kernel adds a run's partials in a fixed order.
+// Every row is written once, by one group: no atomics.
 #include "common.hpp"
 #include "radix_sort.hpp"
 #include "rows.hpp"
@@ -83,10 +84,13 @@ int launch_fwd(const void* table, int64_t rows, int d, const int64_t* tokens, in
 
 // ------------------------------------------------------------------ gradient
 
-// Sorted positions per chunk: long chunks leave few partial sums, short ones
-// give enough lane groups when there are few positions.
-constexpr int kLongChunk = 64, kShortChunk = 16;
-int chunk_len(int64_t n) { return n >= 65536 ? kLongChunk : kShortChunk; }
+// Sorted positions per lane group of 2^g_log2 lanes: kBatch rows in flight at
+// once, more batches where a block has few groups (wide rows) and there are
+// positions enough, so that a block still spans at least 256 of them.
+constexpr int kBatch = 16;
+int chunk_len(int64_t n, int g_log2) { return n >= 65536 && (1 << g_log2) > kBatch ? 1 << g_log2 : kBatch; }
+int block_span(int64_t n, int g_log2) { return (256 >> g_log2) * chunk_len(n, g_log2); }
+constexpr int kMinSpan = 4 * kBatch;  // four groups of 64 lanes
 
 __device__ __forceinline__ uint32_t token_key(int64_t t, int64_t rows) {
   return (uint32_t)(t >= 0 && t < rows ? t : rows);
@@ -226,8 +230,10 @@ __device__ __forceinline__ void put_part(float* p, const float (&acc)[VE]) {
 }
 
 // One lane group per chunk and column slice (blockIdx.y).  The block's keys
-// and positions come through LDS; 2 U rows are in flight per group.
-template <class T, int VE, int U>
+// and positions come through LDS; a batch's rows are all on their way before
+// the first is added (a store of a finished row between loads would make the
+// next wait one for the store).
+template <class T, int VE>
 __global__ __launch_bounds__(256) void token_chunk_kernel(const uint32_t* __restrict__ keys,
                                                           const int32_t* __restrict__ vals, int n, uint32_t rows,
                                                           int chunk_len, const T* __restrict__ dout, int64_t ld, int d,
@@ -235,90 +241,119 @@ __global__ __launch_bounds__(256) void token_chunk_kernel(const uint32_t* __rest
                                                           float* __restrict__ dtable, float* __restrict__ head,
                                                           float* __restrict__ tail) {
   extern __shared__ uint32_t staged[];  // keys, then positions, of the block's chunks
-  const int GL = 1 << g_log2, gl = threadIdx.x & (GL - 1);
-  const int span = (256 >> g_log2) * chunk_len;
+  __shared__ float heads[256][VE], tails[256][VE];
+  __shared__ uint8_t through[64];  // group: its chunk lies within one run that began before it and goes on
+  const int GL = 1 << g_log2, gl = threadIdx.x & (GL - 1), groups = 256 >> g_log2;
+  const int span = groups * chunk_len;
   const int64_t b0 = (int64_t)blockIdx.x * span;
   for (int i = threadIdx.x; i < span; i += 256) {
     const bool in = b0 + i < n;
     staged[i] = in ? keys[b0 + i] : rows;
     staged[span + i] = in ? (uint32_t)vals[b0 + i] : 0u;
   }
-  const int grp = threadIdx.x >> g_log2;
-  const int64_t chunk = (int64_t)blockIdx.x * (256 >> g_log2) + grp, c0 = chunk * chunk_len;
-  // the keys on either side (no key is ~0)
-  const uint32_t before = c0 > 0 && c0 < n ? keys[c0 - 1] : ~0u;
-  const uint32_t after = c0 + chunk_len < n ? keys[c0 + chunk_len] : ~0u;
+  // the keys on either side of the block (no key is ~0)
+  const uint32_t block_before = b0 > 0 ? keys[b0 - 1] : ~0u;
+  const uint32_t block_after = b0 + span < n ? keys[b0 + span] : ~0u;
   __syncthreads();
+  const int grp = threadIdx.x >> g_log2;
   const uint32_t* ck = staged + grp * chunk_len;
   const uint32_t* cp = ck + span;
+  const uint32_t before = grp > 0 ? ck[-1] : block_before;
+  const uint32_t after = grp < groups - 1 ? ck[chunk_len] : block_after;
   uint32_t cur = ck[0];
-  if (cur >= rows) return;  // padding, or past the end
-  bool open = before == cur;  // the run began before this chunk
+  const bool live = cur < rows;  // else padding, or past the end
+  const bool entered = live && before == cur;  // the first run began before this chunk
+  bool open = entered;
   const int col = ((int)blockIdx.y * GL + gl) * VE;
   const bool on = col < d;
   float acc[VE];
 #pragma unroll
   for (int c = 0; c < VE; ++c) acc[c] = 0.f;
+  auto keep = [&](float (*to)[VE]) {
+#pragma unroll
+    for (int c = 0; c < VE; ++c) to[threadIdx.x][c] = acc[c];
+  };
   auto close = [&]() {  // the run of `cur` ends here
-    if (!on) return;
-    if (open) put_part<VE>(head + chunk * d + col, acc);
-    else put_row<VE>(dtable + (int64_t)cur * d + col, acc, scale, add);
+    if (open) keep(heads);
+    else if (on) put_row<VE>(dtable + (int64_t)cur * d + col, acc, scale, add);
   };
-  Piece<T, VE> in[2][U];
-  auto fetch = [&](int q0, Piece<T, VE> (&to)[U]) {
+  if (live) {
+    for (int q0 = 0; q0 < chunk_len; q0 += kBatch) {
+      Piece<T, VE> in[kBatch];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (on && q0 + u < chunk_len && ck[q0 + u] < rows) to[u].load(dout + (int64_t)cp[q0 + u] * ld + col);
-  };
-  auto take = [&](int q0, const Piece<T, VE> (&from)[U]) {
+      for (int u = 0; u < kBatch; ++u)
+        if (on && ck[q0 + u] < rows) in[u].load(dout + (int64_t)cp[q0 + u] * ld + col);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint32_t key = q0 + u < chunk_len ? ck[q0 + u] : rows;
-      if (key >= rows) continue;
-      if (key != cur) {
-        close();
-        cur = key;
-        open = false;
+      for (int u = 0; u < kBatch; ++u) {
+        const uint32_t key = ck[q0 + u];
+        if (key >= rows) break;
+        if (key != cur) {
+          close();
+          cur = key;
+          open = false;
 #pragma unroll
-        for (int c = 0; c < VE; ++c) acc[c] = 0.f;
-      }
-      if (on) {
-        float v[VE];
-        from[u].get(v);
+          for (int c = 0; c < VE; ++c) acc[c] = 0.f;
+        }
+        if (on) {
+          float v[VE];
+          in[u].get(v);
 #pragma unroll
-        for (int c = 0; c < VE; ++c) acc[c] += v[c];
+          for (int c = 0; c < VE; ++c) acc[c] += v[c];
+        }
       }
     }
-  };
-  fetch(0, in[0]);
-  for (int q0 = 0; q0 < chunk_len; q0 += 2 * U) {
-    fetch(q0 + U, in[1]);
-    take(q0, in[0]);
-    fetch(q0 + 2 * U, in[0]);
-    take(q0 + U, in[1]);
   }
-  if (after != cur) close();
-  else if (on) put_part<VE>((open ? head : tail) + chunk * d + col, acc);
+  const bool leaves = live && after == cur;  // the last run goes on
+  if (live) {
+    if (!leaves) close();
+    else keep(open ? heads : tails);
+  }
+  if (gl == 0) through[grp] = leaves && open;
+  __syncthreads();
+  // the group where a run begins adds up its chunks of this block; so does
+  // the first group, for a run that comes from the block before
+  const bool begins = leaves && !open;
+  if (!begins && !(grp == 0 && entered)) return;
+  // (one group may do both: the run that enters it and the one that leaves it)
+  for (int which = 0; which < 2; ++which) {
+    const bool enters = which == 0;
+    if (enters ? !(grp == 0 && entered) : !begins) continue;
+    int at = grp;
+    float v[VE];
+#pragma unroll
+    for (int c = 0; c < VE; ++c) v[c] = (enters ? heads : tails)[threadIdx.x][c];
+    bool on_we_go = enters ? through[0] != 0 : true;
+    while (on_we_go && at + 1 < groups) {
+      ++at;
+#pragma unroll
+      for (int c = 0; c < VE; ++c) v[c] += heads[(at << g_log2) + gl][c];
+      on_we_go = through[at] != 0;
+    }
+    if (!on) continue;
+    if (enters) put_part<VE>(head + (int64_t)blockIdx.x * d + col, v);
+    else if (on_we_go) put_part<VE>(tail + (int64_t)blockIdx.x * d + col, v);
+    else put_row<VE>(dtable + (int64_t)cur * d + col, v, scale, add);
+  }
 }
 
-// One wave per chunk whose last run begins in it and goes on: tail of this
-// chunk plus the heads of the chunks that the run reaches, the wave's lane
-// groups taking every groups-th partial, then added across groups.  Runs of
-// more than kJoinWave partials (a popular token's) are taken by the whole
-// block, one after the other.
-constexpr int kJoinThreads = 1024, kJoinWaves = kJoinThreads / 64, kJoinWave = 64, kJoinFlight = 8;
+// One wave per block of the sum kernel whose last run begins in it and goes
+// on: its tail plus the heads of the blocks that the run reaches, the wave's
+// lane groups taking every groups-th partial, then added across groups.  Runs
+// of more than kJoinWave partials (a popular token's) are taken by the whole
+// workgroup, one after the other.
+constexpr int kJoinThreads = 256, kJoinWaves = kJoinThreads / 64, kJoinWave = 64, kJoinFlight = 8;
 
-// partials first, first + step, ... up to m of the run that begins in `chunk`
+// partials first, first + step, ... up to m of the run that begins in `block`
 template <int VE>
 __device__ __forceinline__ void add_partials(const float* __restrict__ head, const float* __restrict__ tail,
-                                             int64_t chunk, int64_t m, int64_t first, int64_t step, int d, int col,
+                                             int64_t block, int64_t m, int64_t first, int64_t step, int d, int col,
                                              float (&acc)[VE]) {
   for (int64_t i0 = first; i0 <= m; i0 += step * kJoinFlight) {
     Piece<float, VE> p[kJoinFlight];
 #pragma unroll
     for (int u = 0; u < kJoinFlight; ++u) {
       const int64_t i = i0 + u * step;
-      if (i <= m) p[u].load((i == 0 ? tail + chunk * d : head + (chunk + i) * d) + col);
+      if (i <= m) p[u].load((i == 0 ? tail + block * d : head + (block + i) * d) + col);
     }
 #pragma unroll
     for (int u = 0; u < kJoinFlight; ++u) {
@@ -333,7 +368,7 @@ __device__ __forceinline__ void add_partials(const float* __restrict__ head, con
 
 template <int VE>
 __global__ __launch_bounds__(kJoinThreads) void token_join_kernel(const uint32_t* __restrict__ keys, int n,
-                                                                  uint32_t rows, int chunk_len, int d, int g_log2,
+                                                                  uint32_t rows, int span, int d, int g_log2,
                                                                   float scale, bool add, float* __restrict__ dtable,
                                                                   const float* __restrict__ head,
                                                                   const float* __restrict__ tail) {
@@ -349,9 +384,9 @@ __global__ __launch_bounds__(kJoinThreads) void token_join_kernel(const uint32_t
       for (int c = 0; c < VE; ++c) acc[c] += __shfl_xor(acc[c], o, 64);
     }
   };
-  const int64_t chunk = (int64_t)blockIdx.x * kJoinWaves + wave;
-  const int64_t c0 = chunk * chunk_len, c1 = c0 + chunk_len;
-  int64_t m = 0;  // chunks after this one that the run reaches
+  const int64_t block = (int64_t)blockIdx.x * kJoinWaves + wave;
+  const int64_t c0 = block * span, c1 = c0 + span;
+  int64_t m = 0;  // blocks after this one that the run reaches
   uint32_t key = rows;
   if (c1 < n) {
     const uint32_t k0 = keys[c0], k1 = keys[c1 - 1], k2 = keys[c1];
@@ -360,7 +395,7 @@ __global__ __launch_bounds__(kJoinThreads) void token_join_kernel(const uint32_t
   }
   if (key < rows) {
     for (;;) {
-      const int64_t p = (chunk + 1 + m + lane) * chunk_len;
+      const int64_t p = (block + 1 + m + lane) * span;
       const uint64_t miss = __ballot(!(p < n && keys[p] == key));
       if (miss) {
         m += __ffsll((long long)miss) - 1;
@@ -374,7 +409,7 @@ __global__ __launch_bounds__(kJoinThreads) void token_join_kernel(const uint32_t
 #pragma unroll
   for (int c = 0; c < VE; ++c) acc[c] = 0.f;
   if (m > 0 && m <= kJoinWave) {
-    if (on) add_partials<VE>(head, tail, chunk, m, grp, groups, d, col, acc);
+    if (on) add_partials<VE>(head, tail, block, m, grp, groups, d, col, acc);
     wave_sum(acc);
     if (on && lane < GL) put_row<VE>(dtable + (int64_t)key * d + col, acc, scale, add);
   }
@@ -416,30 +451,29 @@ void token_layout(int64_t n, int d, TokenLayout* L) {
     cv.take<char>(bytes);
     return cv.used - bytes;
   };
-  const int64_t m = n > 0 ? n : 1, tiles = ceil_div(m, TILE), chunks = ceil_div(m, chunk_len(m));
+  const int64_t m = n > 0 ? n : 1, tiles = ceil_div(m, TILE), blocks = ceil_div(m, kMinSpan);
   for (int i = 0; i < 2; ++i) L->keys[i] = take(4 * (size_t)m);
   for (int i = 0; i < 2; ++i) L->vals[i] = take(4 * (size_t)m);
   L->counts = take(4 * (size_t)(1 << kMaxDigitBits) * tiles);
   L->sums = take(4 * (size_t)(1 << kMaxDigitBits) * ceil_div(tiles, kChunk));
   L->offsets = take(4 * (size_t)(1 << kMaxDigitBits) * tiles);
-  L->head = take(4 * (size_t)chunks * d);
-  L->tail = take(4 * (size_t)chunks * d);
+  L->head = take(4 * (size_t)blocks * d);
+  L->tail = take(4 * (size_t)blocks * d);
   L->bytes = cv.bytes();
 }
 
 template <class T, int VE>
 int launch_bwd(const uint32_t* keys, const int32_t* vals, int n, uint32_t rows, const void* dout, int64_t ld, int d,
                float scale, bool add, float* dtable, float* head, float* tail, hipStream_t stream) {
-  const int len = chunk_len(n);
-  const int64_t chunks = ceil_div(n, len);
-  const int g = group_log2(d / VE) < 2 ? 2 : group_log2(d / VE);  // at most 64 groups' keys in a block's LDS
+  const int g = group_log2(d / VE) < 2 ? 2 : group_log2(d / VE);  // at most 64 groups per block
   const unsigned slices = (unsigned)ceil_div(d / VE, 1 << g);
-  hipLaunchKernelGGL((token_chunk_kernel<T, VE, 8>), dim3((unsigned)ceil_div(chunks, 256 >> g), slices), dim3(256),
-                     8u * (256 >> g) * len, stream, keys, vals, n, rows, len, static_cast<const T*>(dout), ld, d, g, scale, add, dtable, head,
-                     tail);
-  if (chunks > 1)
-    hipLaunchKernelGGL((token_join_kernel<VE>), dim3((unsigned)ceil_div(chunks, kJoinWaves), slices), dim3(kJoinThreads), 0,
-                       stream, keys, n, rows, len, d, g, scale, add, dtable, head, tail);
+  const int len = chunk_len(n, g), span = block_span(n, g);
+  const int64_t blocks = ceil_div(n, span);
+  hipLaunchKernelGGL((token_chunk_kernel<T, VE>), dim3((unsigned)blocks, slices), dim3(256), 8u * span, stream, keys,
+                     vals, n, rows, len, static_cast<const T*>(dout), ld, d, g, scale, add, dtable, head, tail);
+  if (blocks > 1)
+    hipLaunchKernelGGL((token_join_kernel<VE>), dim3((unsigned)ceil_div(blocks, kJoinWaves), slices), dim3(kJoinThreads),
+                       0, stream, keys, n, rows, span, d, g, scale, add, dtable, head, tail);
   return launch_status();
 }
 
