@@ -26,6 +26,46 @@ constexpr int kMaxDigits = 512;        // buckets of a digit of at most 9 bits
 // contiguous span.
 constexpr int kChunk = 64;  // tiles per chunk of the offset scan
 
+// Memory to clear beside the sort: its kernels have few blocks and wait on
+// each other's counts, so a clear of memory that the sort does not touch
+// costs little in extra blocks of the same launches (blocks first .. of the
+// grid's x).
+struct Clear {
+  float4* p = nullptr;
+  int64_t n = 0;  // float4s
+  unsigned first = 0xffffffffu;
+  __device__ __forceinline__ bool mine() const { return blockIdx.x >= first; }
+  __device__ __forceinline__ void run() const {
+    const int64_t blocks = (int64_t)(gridDim.x - first) * gridDim.y;
+    const int64_t b = (int64_t)(blockIdx.x - first) * gridDim.y + blockIdx.y;
+    for (int64_t i = b * blockDim.x + threadIdx.x; i < n; i += blocks * blockDim.x) p[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+};
+constexpr int kClearPerBlock = 256 * 16;  // float4s
+
+// Splits a clear over `launches` launches: takes the next share and widens
+// the grid's x for it.
+struct ClearParts {
+  float4* p = nullptr;
+  int64_t n = 0;
+  int launches = 1;
+  Clear next(dim3* grid) {
+    Clear c;
+    const int64_t share = launches > 1 ? ceil_div(n, launches) : n;
+    --launches;
+    c.first = grid->x;
+    c.p = p;
+    c.n = share;
+    if (share > 0) {
+      const int64_t blocks = ceil_div(ceil_div(share, kClearPerBlock), grid->y);
+      grid->x += (unsigned)(blocks < 65536 ? blocks : 65536);
+      p += share;
+      n -= share;
+    }
+    return c;
+  }
+};
+
 // block-wide exclusive scan of one value per thread (256 threads); returns
 // the exclusive prefix and writes the block total to *total
 __device__ __forceinline__ uint32_t block_exclusive_scan(uint32_t v, uint32_t* s_wave, uint32_t* total) {
@@ -57,9 +97,10 @@ __device__ __forceinline__ int tile_pos(int wave, int i, int lane) { return wave
 // counts[tile][digit] of one pass (per-wave LDS counters).
 template <int DB>
 __global__ __launch_bounds__(RT) void tile_hist_kernel(const uint32_t* __restrict__ keys, int n, int shift,
-                                                       uint32_t* __restrict__ counts, int tiles) {
+                                                       uint32_t* __restrict__ counts, Clear clear) {
   constexpr int NB = 1 << DB;
   __shared__ uint32_t cnt[4][NB];
+  if (clear.mine()) return clear.run();
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   for (int i = tid; i < 4 * NB; i += RT) (&cnt[0][0])[i] = 0u;
   __syncthreads();
@@ -83,9 +124,10 @@ __global__ __launch_bounds__(RT) void tile_hist_kernel(const uint32_t* __restric
 // (chunk, 64-digit group), lane = digit, wave w takes 16 of the 64 tiles.
 template <int DB>
 __global__ __launch_bounds__(RT) void chunk_sum_kernel(const uint32_t* __restrict__ counts, int tiles,
-                                                       uint32_t* __restrict__ sums) {
+                                                       uint32_t* __restrict__ sums, Clear clear) {
   constexpr int NB = 1 << DB;
   __shared__ uint32_t part[4][64];
+  if (clear.mine()) return clear.run();
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int dg = blockIdx.y * 64 + lane;
   const int t0 = blockIdx.x * kChunk + wave * (kChunk / 4);
@@ -121,11 +163,12 @@ __device__ __forceinline__ uint32_t column_sum(const uint32_t* __restrict__ col,
 template <int DB>
 __global__ __launch_bounds__(RT) void tile_offset_kernel(const uint32_t* __restrict__ counts,
                                                          const uint32_t* __restrict__ sums, int tiles,
-                                                         uint32_t* __restrict__ offsets) {
+                                                         uint32_t* __restrict__ offsets, Clear clear) {
   constexpr int NB = 1 << DB, DPT = NB / RT;
   __shared__ uint32_t s_wave[4];
   __shared__ uint32_t dstart[NB];
   __shared__ uint32_t part[4][64];
+  if (clear.mine()) return clear.run();
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int chunks = (tiles + kChunk - 1) / kChunk;
   const int chunk = blockIdx.x;
@@ -170,7 +213,7 @@ __global__ __launch_bounds__(RT) void tile_offset_kernel(const uint32_t* __restr
 template <int DB>
 __global__ __launch_bounds__(RT) void scatter_kernel(const uint32_t* __restrict__ kin, const int32_t* __restrict__ vin,
                                                      uint32_t* __restrict__ kout, int32_t* __restrict__ vout, int n,
-                                                     int shift, const uint32_t* __restrict__ offsets, int tiles) {
+                                                     int shift, const uint32_t* __restrict__ offsets, Clear clear) {
   constexpr int NB = 1 << DB, DPT = NB / RT;  // digits per thread (contiguous)
   __shared__ uint32_t wcnt[4][NB];           // per-wave counts, then per-wave offsets
   __shared__ uint32_t lstart[NB];            // tile-local start of each digit
@@ -178,6 +221,7 @@ __global__ __launch_bounds__(RT) void scatter_kernel(const uint32_t* __restrict_
   __shared__ uint32_t lkeys[TILE];
   __shared__ int32_t lvals[TILE];
   __shared__ uint32_t s_wave[4];
+  if (clear.mine()) return clear.run();
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int tile = blockIdx.x;
   for (int i = tid; i < 4 * NB; i += RT) (&wcnt[0][0])[i] = 0u;
@@ -275,21 +319,27 @@ SortPlan sort_plan(int key_bits, int max_digit_bits) {
 
 // Every pass of the plan over keys[0] / vals[0]; the sorted pairs end in
 // buffer passes % 2, which is returned.  counts and offsets hold tiles
-// rows of 1 << digit_bits words, sums one such row per kChunk tiles.
+// rows of 1 << digit_bits words, sums one such row per kChunk tiles.  `clear`
+// is what is left to clear, over 4 launches a pass.
 int launch_sort(const SortPlan& plan, uint32_t* const (&keys)[2], int32_t* const (&vals)[2], uint32_t* counts,
-                uint32_t* sums, uint32_t* offsets, int n, hipStream_t stream) {
+                uint32_t* sums, uint32_t* offsets, int n, hipStream_t stream, ClearParts clear = ClearParts()) {
   const unsigned tiles = (unsigned)ceil_div(n, TILE);
+  const dim3 tile_grid(tiles);
   const dim3 chunk_grid((unsigned)ceil_div(tiles, kChunk), (unsigned)((1 << plan.digit_bits) / 64));
+  clear.launches = 4 * plan.passes;
   int cur = 0;
   for (int pass = 0; pass < plan.passes; ++pass) {
     const int shift = pass * plan.digit_bits;
+    dim3 grid[4] = {tile_grid, chunk_grid, chunk_grid, tile_grid};
+    Clear c[4];
+    for (int i = 0; i < 4; ++i) c[i] = clear.next(&grid[i]);
 #define DLRM_PASS(DB)                                                                                               \
-  hipLaunchKernelGGL(tile_hist_kernel<DB>, dim3(tiles), dim3(RT), 0, stream, keys[cur], n, shift, counts,          \
-                     (int)tiles);                                                                                  \
-  hipLaunchKernelGGL(chunk_sum_kernel<DB>, chunk_grid, dim3(RT), 0, stream, counts, (int)tiles, sums);             \
-  hipLaunchKernelGGL(tile_offset_kernel<DB>, chunk_grid, dim3(RT), 0, stream, counts, sums, (int)tiles, offsets);  \
-  hipLaunchKernelGGL(scatter_kernel<DB>, dim3(tiles), dim3(RT), 0, stream, keys[cur], vals[cur], keys[cur ^ 1],    \
-                     vals[cur ^ 1], n, shift, offsets, (int)tiles)
+  hipLaunchKernelGGL(tile_hist_kernel<DB>, grid[0], dim3(RT), 0, stream, keys[cur], n, shift, counts, c[0]);       \
+  hipLaunchKernelGGL(chunk_sum_kernel<DB>, grid[1], dim3(RT), 0, stream, counts, (int)tiles, sums, c[1]);          \
+  hipLaunchKernelGGL(tile_offset_kernel<DB>, grid[2], dim3(RT), 0, stream, counts, sums, (int)tiles, offsets,      \
+                     c[2]);                                                                                        \
+  hipLaunchKernelGGL(scatter_kernel<DB>, grid[3], dim3(RT), 0, stream, keys[cur], vals[cur], keys[cur ^ 1],        \
+                     vals[cur ^ 1], n, shift, offsets, c[3])
     if (plan.digit_bits == 10) {
       DLRM_PASS(10);
     } else if (plan.digit_bits == 9) {

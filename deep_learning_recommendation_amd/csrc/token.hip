@@ -95,25 +95,19 @@ constexpr int kMinSpan = 4 * kBatch;  // four groups of 64 lanes
 __device__ __forceinline__ uint32_t token_key(int64_t t, int64_t rows) {
   return (uint32_t)(t >= 0 && t < rows ? t : rows);
 }
-__device__ __forceinline__ void zero_rows(float4* zero, int64_t zero4, int64_t at, int64_t step) {
-  for (int64_t i = at; i < zero4; i += step) zero[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-}
 
 // Keys (the token, or `rows` for one that names no row: those sort last) and
-// positions; and, unless the gradient is added to what the table gradient
-// holds, +0 into every row of it.
+// positions.
 __global__ __launch_bounds__(256) void token_keys_kernel(const int64_t* __restrict__ tokens, int n, int64_t rows,
-                                                         uint32_t* __restrict__ keys, int32_t* __restrict__ vals,
-                                                         float4* __restrict__ zero, int64_t zero4) {
-  const int64_t at = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, step = (int64_t)gridDim.x * blockDim.x;
-  for (int64_t i = at; i < n; i += step) {
+                                                         uint32_t* __restrict__ keys, int32_t* __restrict__ vals) {
+  const int64_t step = (int64_t)gridDim.x * blockDim.x;
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += step) {
     keys[i] = token_key(tokens[i], rows);
     vals[i] = (int32_t)i;
   }
-  zero_rows(zero, zero4, at, step);
 }
 
-// Few tokens: block 0 does the whole sort in LDS (the ranking of
+// Few tokens: one block does the whole sort in LDS (the ranking of
 // scatter_kernel, digit by digit) while the others clear the table gradient.
 // One launch instead of the nine of two global passes, whose time would all
 // be launches.
@@ -121,18 +115,13 @@ constexpr int kSmallThreads = 1024, kSmallItems = 8, kSmallMax = kSmallThreads *
 __global__ __launch_bounds__(kSmallThreads) void token_sort_small_kernel(const int64_t* __restrict__ tokens, int n,
                                                                          int64_t rows, int key_bits,
                                                                          uint32_t* __restrict__ keys,
-                                                                         int32_t* __restrict__ vals,
-                                                                         float4* __restrict__ zero, int64_t zero4) {
+                                                                         int32_t* __restrict__ vals, Clear clear) {
   constexpr int NB = 256, W = kSmallThreads / 64;
   __shared__ uint32_t lk[kSmallMax];
   __shared__ int32_t lv[kSmallMax];
   __shared__ uint32_t cnt[W][NB];
   __shared__ uint32_t tot[NB / 64];
-  if (blockIdx.x > 0) {  // there when zero4 > 0
-    zero_rows(zero, zero4, (int64_t)(blockIdx.x - 1) * kSmallThreads + threadIdx.x,
-              (int64_t)(gridDim.x - 1) * kSmallThreads);
-    return;
-  }
+  if (clear.mine()) return clear.run();
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const uint64_t below = (lane == 0) ? 0ull : (~0ull >> (64 - lane));
   const int items = (n + kSmallThreads - 1) / kSmallThreads;  // wave w holds positions (w items + i) 64 + lane
@@ -531,22 +520,24 @@ extern "C" int dlrm_token_embed_bwd(const int64_t* tokens, int64_t n, const void
   int32_t* const vals[2] = {reinterpret_cast<int32_t*>(w + L.vals[0]), reinterpret_cast<int32_t*>(w + L.vals[1])};
   auto u32 = [&](size_t at) { return reinterpret_cast<uint32_t*>(w + at); };
   const bool add = accumulate != 0;
-  const int64_t zero4 = add ? 0 : rows * d / 4;
-  const int64_t most = n > zero4 ? n : zero4;
-  if (most == 0) return DLRM_OK;
-  float4* zero = reinterpret_cast<float4*>(dtable);
+  // unless the gradient is added to it, dtable starts from +0: cleared beside the sort
+  ClearParts clear;
+  clear.p = reinterpret_cast<float4*>(dtable);
+  clear.n = add ? 0 : rows * d / 4;
+  if (n == 0 && clear.n == 0) return DLRM_OK;
   int cur = 0;
   if (n <= kSmallMax) {
-    const int64_t blocks = 1 + ceil_div(zero4, kSmallThreads * 4);
-    hipLaunchKernelGGL(token_sort_small_kernel, dim3((unsigned)(blocks < 1024 ? blocks : 1024)), dim3(kSmallThreads), 0,
-                       stream, tokens, (int)n, rows, bits_for(rows), keys[0], vals[0], zero, zero4);
+    dim3 grid(1);
+    const Clear c = clear.next(&grid);
+    hipLaunchKernelGGL(token_sort_small_kernel, grid, dim3(kSmallThreads), 0, stream, tokens, (int)n, rows,
+                       bits_for(rows), keys[0], vals[0], c);
     if (n == 0) return launch_status();
   } else {
-    const int64_t blocks = ceil_div(most, 256);
+    const int64_t blocks = ceil_div(n, 256);
     hipLaunchKernelGGL(token_keys_kernel, dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256), 0, stream, tokens,
-                       (int)n, rows, keys[0], vals[0], zero, zero4);
+                       (int)n, rows, keys[0], vals[0]);
     cur = launch_sort(sort_plan(bits_for(rows), kMaxDigitBits), keys, vals, u32(L.counts), u32(L.sums), u32(L.offsets),
-                      (int)n, stream);
+                      (int)n, stream, clear);
   }
   float* head = reinterpret_cast<float*>(w + L.head);
   float* tail = reinterpret_cast<float*>(w + L.tail);
