@@ -170,8 +170,18 @@ struct Mat<float> {
   }
 };
 
-// decay^e for e >= 0, from l = log2(decay) (decay 0: l = -inf)
-__device__ __forceinline__ float decay_pow(float l, int e) { return e == 0 ? 1.f : exp2f(l * (float)e); }
+// log2(decay), bounded so that decay 0 has decay^0 = 1 and decay^e = 0 from e = 1 on
+__device__ __forceinline__ float log2_decay(float decay) { return fmaxf(log2f(decay), -256.f); }
+// decay^e for e >= 0
+__device__ __forceinline__ float decay_pow(float l, float e) { return __builtin_amdgcn_exp2f(l * e); }
+
+// A copy of x that the compiler does not see through: what is computed from it
+// stays where it is, instead of in registers across a loop.
+template <class V>
+__device__ __forceinline__ V local_copy(V x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
 
 // What a workgroup holds: VS columns of the output and of the state (a
 // slice), the state's DK rows spread over the four waves.
@@ -186,7 +196,13 @@ struct Shape {
   // at a time in 8-byte pieces
   static constexpr int kPK = DK + (DK == 128 && sizeof(T) == 2 ? 16 : 16 / (int)sizeof(T));
   static constexpr int kPV = VS + 4;
-  static constexpr int kBytes = (kC * kPK + kC * kPV + VS * kPK) * (int)sizeof(T) + (VS + 4) * 4;
+  static constexpr int kTileBytes = (kC * kPK + kC * kPV + VS * kPK) * (int)sizeof(T);
+  static constexpr int kBytes = kTileBytes + (VS + 4) * 4;
+  // a state on its way between memory and registers uses the tiles' LDS
+  static constexpr int kPS = VS + 4;
+  static_assert(DK * kPS * 4 <= kTileBytes, "a state fits the tiles' LDS");
+  // waves per SIMD that the LDS of whole workgroups leaves room for
+  static constexpr int kWaves = kBytes > 80 * 1024 ? 1 : kBytes > 53 * 1024 ? 2 : kBytes > 40 * 1024 ? 3 : 4;
   static constexpr int kBlob = kMW * kNW * 4;  // state floats per thread
   // column of the slice that index m of tile j stands for: a lane's tiles
   // then hold VS / 4 consecutive columns of a row of the output
@@ -200,10 +216,12 @@ struct State {
   f32x4 t[Sh::kMW][Sh::kNW];
 
   static __device__ __forceinline__ int row(int i) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     return 16 * ((wave % Sh::kWM) * Sh::kMW + i) + 4 * (lane >> 4);
   }
-  static __device__ __forceinline__ int tile(int j) { return (threadIdx.x >> 6) / Sh::kWM * Sh::kNW + j; }
+  static __device__ __forceinline__ int tile(int j) {
+    return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) / Sh::kWM * Sh::kNW + j;
+  }
 
   __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -211,33 +229,54 @@ struct State {
 #pragma unroll
       for (int j = 0; j < Sh::kNW; ++j) t[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
-  // p: one head's [dk][dv] (flip: [dv][dk]) matrix
+  // p: one head's [dk][dv] (flip: [dv][dk]) matrix.  Rows of the matrix go
+  // through LDS, so that memory sees 16 bytes per lane along them; a
+  // transposed one has four consecutive elements per lane already.
   template <class F>
-  static __device__ __forceinline__ void each(int col0, int dk, int dv, F f) {
+  static __device__ __forceinline__ void each(F f) {
 #pragma unroll
     for (int i = 0; i < Sh::kMW; ++i)
 #pragma unroll
-      for (int j = 0; j < Sh::kNW; ++j) {
-        const int r = row(i), c = col0 + Sh::column(threadIdx.x & 15, tile(j));
-        if (r < dk && c < dv) f(i, j, r, c);
-      }
+      for (int j = 0; j < Sh::kNW; ++j) f(i, j, row(i), Sh::column(threadIdx.x & 15, tile(j)));
   }
-  __device__ __forceinline__ void load(const float* p, bool flip, int col0, int dk, int dv) {
-    clear();
-    each(col0, dk, dv, [&](int i, int j, int r, int c) {
-      if (flip) t[i][j] = *reinterpret_cast<const f32x4*>(p + (int64_t)c * dk + r);
-      else
+  __device__ __forceinline__ void load(const float* p, bool flip, int col0, int dk, int dv, float* lds) {
+    if (flip) {
+      each([&](int i, int j, int r, int c) {
+        t[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (r < dk && col0 + c < dv) t[i][j] = *reinterpret_cast<const f32x4*>(p + (int64_t)(col0 + c) * dk + r);
+      });
+      return;
+    }
+    for (int e = threadIdx.x; e < DK * (VS / 4); e += kThreads) {
+      const int r = e / (VS / 4), c = e % (VS / 4) * 4;
+      f32x4 v{0.f, 0.f, 0.f, 0.f};
+      if (r < dk && col0 + c < dv) v = *reinterpret_cast<const f32x4*>(p + r * dv + col0 + c);
+      *reinterpret_cast<f32x4*>(lds + r * Sh::kPS + c) = v;
+    }
+    __syncthreads();
+    each([&](int i, int j, int r, int c) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) t[i][j][e] = p[(r + e) * dv + c];
+      for (int e = 0; e < 4; ++e) t[i][j][e] = lds[(r + e) * Sh::kPS + c];
     });
   }
-  __device__ __forceinline__ void store(float* p, bool flip, int col0, int dk, int dv) const {
-    each(col0, dk, dv, [&](int i, int j, int r, int c) {
-      if (flip) *reinterpret_cast<f32x4*>(p + (int64_t)c * dk + r) = t[i][j];
-      else
+  __device__ __forceinline__ void store(float* p, bool flip, int col0, int dk, int dv, float* lds) const {
+    if (flip) {
+      each([&](int i, int j, int r, int c) {
+        if (r < dk && col0 + c < dv) *reinterpret_cast<f32x4*>(p + (int64_t)(col0 + c) * dk + r) = t[i][j];
+      });
+      return;
+    }
+    __syncthreads();
+    each([&](int i, int j, int r, int c) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) p[(r + e) * dv + c] = t[i][j][e];
+      for (int e = 0; e < 4; ++e) lds[(r + e) * Sh::kPS + c] = t[i][j][e];
     });
+    __syncthreads();
+    for (int e = threadIdx.x; e < DK * (VS / 4); e += kThreads) {
+      const int r = e / (VS / 4), c = e % (VS / 4) * 4;
+      if (r < dk && col0 + c < dv)
+        *reinterpret_cast<f32x4*>(p + r * dv + col0 + c) = *reinterpret_cast<const f32x4*>(lds + r * Sh::kPS + c);
+    }
   }
   // a segment's state in the workspace: 16 bytes per thread and tile
   __device__ __forceinline__ void load_blob(const float* p) {
@@ -261,18 +300,18 @@ struct Plan {
   const int64_t* offsets;
   const float* decay;
   float* blobs;     // segments > 1: a state per (segment, slice and role, history and head)
-  int64_t units;    // B * H
-  int H, slices, inner;  // inner = slices * roles
+  unsigned units;   // B * H
+  unsigned H, slices, inner;  // inner = slices * roles
   int segments;
   int64_t seg_len;  // rows per segment, a multiple of kC
   Roles roles;
 };
 // The slices and roles of a unit read the same rows: they are eight blocks
 // apart, on one XCD and next to each other in time.
-__device__ __forceinline__ bool locate(const Plan& p, int64_t units, int64_t* unit, int* in) {
-  const int64_t b = blockIdx.x, span = 8 * (int64_t)p.inner;
-  *unit = b / span * 8 + (b & 7);
-  *in = (int)((b % span) >> 3);
+__device__ __forceinline__ bool locate(const Plan& p, unsigned units, unsigned* unit, unsigned* in) {
+  const unsigned k = blockIdx.x >> 3;
+  *unit = k / p.inner * 8 + (blockIdx.x & 7);
+  *in = k % p.inner;
   return *unit < units;
 }
 
@@ -285,7 +324,8 @@ __device__ __forceinline__ bool locate(const Plan& p, int64_t units, int64_t* un
 // K and V of the next chunk are on their way to registers meanwhile; q goes
 // from memory straight to fragments.  ONLY_STATE: only S, from zero.
 template <class T, int DK, int VS, bool ONLY_STATE>
-__global__ __launch_bounds__(kThreads) void linattn_kernel(Plan plan) {
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(Shape<T, DK, VS>::kWaves))) void linattn_kernel(
+    Plan plan) {
   using M = Mat<T>;
   using Sh = Shape<T, DK, VS>;
   using Frag = typename M::Frag;
@@ -294,18 +334,19 @@ __global__ __launch_bounds__(kThreads) void linattn_kernel(Plan plan) {
   T* Ks = reinterpret_cast<T*>(smem);
   T* Vs = Ks + kC * PK;
   T* Ss = Vs + kC * PV;
-  int* first_bad = reinterpret_cast<int*>(Ss + VS * PK);  // per column, and any: [VS]
+  int* first_bad = reinterpret_cast<int*>(Ss + VS * PK);  // per column of V
+  int* bad_chunk = first_bad + VS;  // whether V has any, for even and odd chunks
+  float* state_lds = reinterpret_cast<float*>(smem);
 
-  const int segs = ONLY_STATE ? plan.segments - 1 : plan.segments;
-  int64_t unit;
-  int in;
+  const unsigned segs = ONLY_STATE ? plan.segments - 1 : plan.segments;
+  unsigned unit, in;
   if (!locate(plan, plan.units * segs, &unit, &in)) return;
   const int64_t bh = unit / segs;
-  const int seg = (int)(unit - bh * segs);
-  const int64_t b = bh / plan.H;
-  const int h = (int)(bh - b * plan.H);
+  const int seg = (int)(unit % segs);
+  const int64_t b = (unsigned)bh / plan.H;
+  const int h = (int)((unsigned)bh % plan.H);
   const Role& role = plan.roles.r[in / plan.slices];
-  const int col0 = in % plan.slices * VS;
+  const int col0 = (int)(in % plan.slices) * VS;
   const int64_t beg = plan.offsets[b], len = plan.offsets[b + 1] - beg;
   const int64_t s0 = seg * plan.seg_len;
   if (seg > 0 && s0 >= len) return;
@@ -316,87 +357,86 @@ __global__ __launch_bounds__(kThreads) void linattn_kernel(Plan plan) {
   constexpr int64_t kBlobFloats = (int64_t)Sh::kBlob * kThreads;
   const int dk = role.dk, dv = role.dv, lead = role.back ? 0 : 1;
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 15, g = lane >> 4;
-  State<T, DK, VS> S;
-  if (ONLY_STATE) S.clear();
-  else if (plan.segments > 1) S.load_blob(plan.blobs + blob * kBlobFloats);
-  else if (role.first) S.load(role.first + bh * dk * dv, role.flip, col0, dk, dv);
-  else S.clear();
-
-  // row t of the segment's time, in memory
-  const int64_t base = role.back ? beg + len - 1 : beg;
-  const int64_t dir = role.back ? -1 : 1;
-  const T* kp = static_cast<const T*>(role.k.p) + h * role.k.hs;
-  const T* vp = static_cast<const T*>(role.v.p) + h * role.v.hs + col0;
-  const T* qp = static_cast<const T*>(role.q.p) + h * role.q.hs;
-  T* op = static_cast<T*>(const_cast<void*>(role.o.p)) + h * role.o.hs + col0;
-
+  const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  // A chunk's 64 places hold its rows at the end: of the last, shorter chunk
+  // of a segment the first 64 - m places stay empty, so that the weights
+  // towards a chunk's end are the same for every chunk.  Place p of the
+  // chunk at c0 is row c0 - (64 - m) + p in time; backwards in time the
+  // places lie in memory from the last to the first.  Addresses are a uniform
+  // base plus an offset of the lane that no chunk changes.
+  const bool back = role.back != 0;
+  auto window = [&](const Strided& x, int64_t start) {  // the window's first row in memory
+    const int64_t row = back ? beg + len - 1 - start - (kC - 1) : beg + start;
+    return static_cast<const char*>(x.p) + (row * x.ts + h * x.hs) * (int64_t)sizeof(T);
+  };
+  auto place = [&](int p) { return back ? kC - 1 - p : p; };
   // a thread's pieces of a chunk of K and V
   constexpr int KP = DK / E, VP = VS / E;                              // pieces per row
   constexpr int KN = kC * KP / kThreads, VN = kC * VP / kThreads;      // per thread
+  constexpr int KR = kThreads / KP, VR = kThreads / VP;                // rows between a thread's pieces
+  const int kr = tid / KP, kc = tid % KP * E, vr = tid / VP, vc = tid % VP * E;
+  const uint32_t koff = (uint32_t)((back ? kC - KR * (KN - 1) - 1 - kr : kr) * (int)role.k.ts + kc) * sizeof(T);
+  const uint32_t voff = (uint32_t)((back ? kC - VR * (VN - 1) - 1 - vr : vr) * (int)role.v.ts + col0 + vc) * sizeof(T);
+  const uint32_t qoff = (uint32_t)(place(16 * wave + n) * (int)role.q.ts + g * (M::kWide / 4)) * sizeof(T);
+  const uint32_t ooff = (uint32_t)(place(16 * wave + n) * (int)role.o.ts + col0 + (VS / 4) * g) * sizeof(T);
   uint4 kreg[KN], vreg[VN];
   auto fetch = [&](int64_t c0) {
-    const int64_t left = s1 - c0;
+    const int empty = s1 - c0 < kC ? kC - (int)(s1 - c0) : 0;
+    const char* k0 = window(role.k, c0 - empty);
+    const char* v0 = window(role.v, c0 - empty);
+    const uint32_t ko = local_copy(koff), vo = local_copy(voff);
 #pragma unroll
     for (int i = 0; i < KN; ++i) {
-      const int e = i * kThreads + tid, r = e / KP, c = e % KP * E;
       kreg[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (r < left && c < dk) kreg[i] = *reinterpret_cast<const uint4*>(kp + (base + dir * (c0 + r)) * role.k.ts + c);
+      const int64_t step = (back ? KN - 1 - i : i) * KR * role.k.ts * (int64_t)sizeof(T);
+      if (kr + i * KR >= empty && kc < dk) kreg[i] = *reinterpret_cast<const uint4*>(k0 + step + ko);
     }
 #pragma unroll
     for (int i = 0; i < VN; ++i) {
-      const int e = i * kThreads + tid, r = e / VP, c = e % VP * E;
       vreg[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (r < left && col0 + c < dv)
-        vreg[i] = *reinterpret_cast<const uint4*>(vp + (base + dir * (c0 + r)) * role.v.ts + c);
+      const int64_t step = (back ? VN - 1 - i : i) * VR * role.v.ts * (int64_t)sizeof(T);
+      if (vr + i * VR >= empty && col0 + vc < dv) vreg[i] = *reinterpret_cast<const uint4*>(v0 + step + vo);
     }
   };
   constexpr int QN = DK / M::kWide;
   Frag qf[QN];
   auto fetch_q = [&](int64_t c0) {
-    const int64_t t = c0 + 16 * wave + n;
+    const int empty = s1 - c0 < kC ? kC - (int)(s1 - c0) : 0;
+    const char* q0 = window(role.q, c0 - empty);
+    const uint32_t qo = local_copy(qoff);
 #pragma unroll
     for (int f = 0; f < QN; ++f) {
-      const int c = f * M::kWide + g * (M::kWide / 4);
       qf[f] = M::zero();
-      if (t < s1 && c < dk) qf[f] = *reinterpret_cast<const Frag*>(qp + (base + dir * t) * role.q.ts + c);
+      if (16 * wave + n >= empty && f * M::kWide + g * (M::kWide / 4) < dk)
+        qf[f] = *reinterpret_cast<const Frag*>(q0 + f * M::kWide * sizeof(T) + qo);
     }
   };
-
-  // weights that every full chunk shares
-  const float l2 = log2f(plan.decay[h]);
-  const float kscale = role.kscale;
-  f32x4 near[2];  // of the tile on the diagonal (0 above it) and of the one before it
-#pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int e = n - 4 * g - r;
-    near[0][r] = e >= 0 ? kscale * decay_pow(l2, e) : 0.f;
-    near[1][r] = kscale * decay_pow(l2, 16 + e);
-  }
-  const float d16 = decay_pow(l2, 16);
-  const float from_state = decay_pow(l2, 16 * wave + n + lead);
-  f32x4 to_end[4];
-  int rows = 0;  // rows of the chunk that to_end stands for
-  auto weights = [&](int m) {
-    rows = m;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int e = m - lead - (16 * i + 4 * g + r);
-        to_end[i][r] = e >= 0 ? kscale * decay_pow(l2, e) : 0.f;
-      }
-  };
-  weights(kC);
 
   if (s0 < s1) {
     fetch(s0);
     if (!ONLY_STATE) fetch_q(s0);
   }
-  for (int64_t c0 = s0; c0 < s1; c0 += kC) {
+  if (tid < 2) bad_chunk[tid] = 0;
+  State<T, DK, VS> S;
+  if (ONLY_STATE) S.clear();
+  else if (plan.segments > 1) S.load_blob(plan.blobs + blob * kBlobFloats);
+  else if (role.first) S.load(role.first + bh * dk * dv, role.flip, col0, dk, dv, state_lds);
+  else S.clear();
+
+  // decays towards a chunk's end, of the last 16 places; an earlier tile's
+  // are these times decay^16 per tile
+  const float l2 = log2_decay(plan.decay[h]);
+  const float kscale = role.kscale;
+  const float d16 = decay_pow(l2, 16.f);
+  f32x4 to_end;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) to_end[r] = kscale * decay_pow(l2, (float)(16 - lead - 4 * g - r));
+
+  int odd = 0;
+  for (int64_t c0 = s0; c0 < s1; c0 += kC, odd ^= 1) {
     const int m = (int)(s1 - c0 < kC ? s1 - c0 : kC);
     __syncthreads();  // every wave is done with the chunk before
-    if (tid < VS + 4) first_bad[tid] = kC;
 #pragma unroll
     for (int i = 0; i < KN; ++i) {
       const int e = i * kThreads + tid;
@@ -420,12 +460,19 @@ __global__ __launch_bounds__(kThreads) void linattn_kernel(Plan plan) {
     }
     // a v that is not finite would reach rows before it as 0 * v: it goes
     // into the products as zero, and its column is NaN from its row on
-    const bool any_bad = __syncthreads_or(bad != 0);
+    if (bad) bad_chunk[odd] = 1;
+    __syncthreads();
+    const bool any_bad = __builtin_amdgcn_readfirstlane(bad_chunk[odd]) != 0;
+    if (tid == 0) bad_chunk[odd ^ 1] = 0;
     if (any_bad) {
+      const int cold = local_copy(tid);
+      if (cold < VS) first_bad[cold] = kC;
+      __syncthreads();
 #pragma unroll
       for (int i = 0; i < VN; ++i) {
-        const int e = i * kThreads + tid;
+        const int e = i * kThreads + cold;
         const uint32_t which = M::bad(vreg[i]);
+#pragma unroll 1
         for (int x = 0; x < E; ++x)
           if ((which >> x) & 1u) {
             Vs[e / VP * PV + e % VP * E + x] = 0;
@@ -437,18 +484,13 @@ __global__ __launch_bounds__(kThreads) void linattn_kernel(Plan plan) {
     if (c0 + kC < s1) fetch(c0 + kC);
 
     f32x4 out[NT];
-    f32x4 p[4];
+    Frag pf[4 / M::kTiles];
+    // per-chunk copies: what is made from them is made again in each chunk,
+    // for kept outside the loop it would cost registers
+    const float tile_decay = local_copy(d16), l = local_copy(l2), lag = local_copy((float)(n - 4 * g));
     if (!ONLY_STATE) {
-#pragma unroll
-      for (int j = 0; j < NT; ++j) out[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int f = 0; f < QN; ++f)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) out[j] = M::mma(M::wide(Ss + (16 * j + n) * PK + f * M::kWide, g), qf[f], out[j]);
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) out[j][r] *= from_state;
+      // the masked, decayed products of this wave's 16 rows with the chunk's
+      f32x4 p[4];
       float far = 1.f;
 #pragma unroll
       for (int i = 3; i >= 0; --i) {
@@ -459,78 +501,94 @@ __global__ __launch_bounds__(kThreads) void linattn_kernel(Plan plan) {
         if (i == wave) {
           // selected, not multiplied: a masked product may not be finite
 #pragma unroll
-          for (int r = 0; r < 4; ++r) p[i][r] = n >= 4 * g + r ? p[i][r] * near[0][r] : 0.f;
+          for (int r = 0; r < 4; ++r)
+            p[i][r] = lag >= (float)r ? p[i][r] * (kscale * decay_pow(l, lag - (float)r)) : 0.f;
         } else {
 #pragma unroll
-          for (int r = 0; r < 4; ++r) p[i][r] *= near[1][r] * far;
-          far *= d16;
+          for (int r = 0; r < 4; ++r) p[i][r] *= kscale * decay_pow(l, lag + (float)(16 - r)) * far;
+          far *= tile_decay;
         }
       }
+#pragma unroll
+      for (int f = 0; f < 4 / M::kTiles; ++f) pf[f] = M::pack(p + f * M::kTiles);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) out[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int f = 0; f < QN; ++f)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) out[j] = M::mma(M::wide(Ss + (16 * j + n) * PK + f * M::kWide, g), qf[f], out[j]);
+      // (an empty place's power may be any; its row is not stored)
+      const float from_state = decay_pow(l, (float)(16 * wave + n - (kC - m) + lead));
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) out[j][r] *= from_state;
       if (c0 + kC < s1) fetch_q(c0 + kC);
     }
-    if (m != rows) weights(m);
-    const float all = decay_pow(l2, m);
+    const float nan = __builtin_nanf("");
+    if (!ONLY_STATE) {
+#pragma unroll
+      for (int f = 0; f < 4 / M::kTiles; ++f) {
+        if (f * M::kTiles > wave) continue;  // above the diagonal
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          out[j] = M::mma(M::template time<PV>(Vs, f, lane, M::time_col(lane, VS / 4) + 4 * j), pf[f], out[j]);
+      }
+      if (16 * wave + n >= kC - m) {
+        char* row = const_cast<char*>(window(role.o, c0 - (kC - m))) + local_copy(ooff);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          f32x4 o = out[j] * role.oscale;
+          if (any_bad) {
+            const int cold = local_copy(lane);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (first_bad[(VS / 4) * (cold >> 4) + 4 * j + r] <= 16 * wave + (cold & 15)) o[r] += nan;
+          }
+          if (col0 + (VS / 4) * g + 4 * j < dv) M::put4(reinterpret_cast<T*>(row) + 4 * j, o);
+        }
+      }
+    }
+    // the state, after the output has left its registers
+    const float all = decay_pow(l2, (float)m);
 #pragma unroll
     for (int i = 0; i < Sh::kMW; ++i)
 #pragma unroll
       for (int j = 0; j < Sh::kNW; ++j)
 #pragma unroll
         for (int r = 0; r < 4; ++r) S.t[i][j][r] *= all;
-
 #pragma unroll
-    for (int f = 0; f < 4 / M::kTiles; ++f) {  // the chunk's rows, a fragment at a time
-      Frag vf[NT];
+    for (int f = 0; f < 4 / M::kTiles; ++f) {
+      Frag vf[Sh::kNW];
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-        vf[j] = M::template time<PV>(Vs, f, lane, M::time_col(lane, VS / 4) + 4 * j);
-      if (!ONLY_STATE && f * M::kTiles <= wave) {
-        const Frag pf = M::pack(p + f * M::kTiles);
+      for (int j = 0; j < Sh::kNW; ++j)
+        vf[j] = M::template time<PV>(Vs, f, lane, M::time_col(lane, VS / 4) + 4 * S.tile(j));
+      f32x4 w[M::kTiles];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) out[j] = M::mma(vf[j], pf, out[j]);
+      for (int x = 0; x < M::kTiles; ++x) {
+        float far = 1.f;
+#pragma unroll
+        for (int i = f * M::kTiles + x; i < 3; ++i) far *= tile_decay;
+        w[x] = to_end * far;
       }
 #pragma unroll
       for (int i = 0; i < Sh::kMW; ++i) {
         const int row0 = 16 * ((wave % Sh::kWM) * Sh::kMW + i);
         const Frag kf = M::template time<PK>(Ks, f, lane, row0 + M::time_col(lane, 4));
-        if constexpr (Sh::kWN == 1) {
-          M::template mma_scaled<Sh::kNW>(kf, to_end + f * M::kTiles, vf, S.t[i]);
-        } else {
-          Frag vw[Sh::kNW];
-#pragma unroll
-          for (int j = 0; j < Sh::kNW; ++j)
-            vw[j] = M::template time<PV>(Vs, f, lane, M::time_col(lane, VS / 4) + 4 * S.tile(j));
-          M::template mma_scaled<Sh::kNW>(kf, to_end + f * M::kTiles, vw, S.t[i]);
-        }
+        M::template mma_scaled<Sh::kNW>(kf, w, vf, S.t[i]);
       }
     }
-    const float nan = __uint_as_float(0x7fc00000u);
     if (any_bad) {
+      const int cold = local_copy(n);
 #pragma unroll
-      for (int i = 0; i < Sh::kMW; ++i)
+      for (int j = 0; j < Sh::kNW; ++j)
+        if (first_bad[Sh::column(cold, S.tile(j))] < kC)
 #pragma unroll
-        for (int j = 0; j < Sh::kNW; ++j)
-          if (first_bad[Sh::column(n, S.tile(j))] < kC) S.t[i][j] = f32x4{nan, nan, nan, nan};
-    }
-    if (!ONLY_STATE) {
-      const int64_t t = c0 + 16 * wave + n;
-      if (t < s1) {
-        float o[VS / 4];
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            o[4 * j + r] = out[j][r] * role.oscale;
-            if (any_bad && first_bad[(VS / 4) * g + 4 * j + r] <= 16 * wave + n) o[4 * j + r] = nan;
-          }
-        T* row = op + (base + dir * t) * role.o.ts;
-#pragma unroll
-        for (int x = 0; x < VS / 4; x += 4)
-          if (col0 + (VS / 4) * g + x < dv) M::put4(row + (VS / 4) * g + x, f32x4{o[x], o[x + 1], o[x + 2], o[x + 3]});
-      }
+          for (int i = 0; i < Sh::kMW; ++i) S.t[i][j] += nan;
     }
   }
   if (ONLY_STATE) S.store_blob(plan.blobs + blob * kBlobFloats);
-  else if (ends && role.last) S.store(role.last + bh * dk * dv, role.flip, col0, dk, dv);
+  else if (ends && role.last) S.store(role.last + bh * dk * dv, role.flip, col0, dk, dv, state_lds);
 }
 
 // The states that enter the segments, in place of those that the segments
@@ -542,20 +600,19 @@ __global__ __launch_bounds__(kThreads) void linattn_scan_kernel(Plan plan) {
   using Sh = Shape<T, DK, VS>;
   using St = State<T, DK, VS>;
   constexpr int64_t kBlobFloats = (int64_t)Sh::kBlob * kThreads;
-  int64_t bh;
-  int in;
-  if (!locate(plan, plan.units, &bh, &in)) return;
-  const int64_t b = bh / plan.H;
-  const int h = (int)(bh - b * plan.H);
+  unsigned unit, in;
+  if (!locate(plan, plan.units, &unit, &in)) return;
+  const int64_t bh = unit, b = unit / plan.H;
+  const int h = (int)(unit % plan.H);
   const Role& role = plan.roles.r[in / plan.slices];
   const int64_t len = plan.offsets[b + 1] - plan.offsets[b];
   const int used = len > 0 ? (int)((len + plan.seg_len - 1) / plan.seg_len) : 1;  // segments that have rows
-  const float l2 = log2f(plan.decay[h]);
-  const float all = exp2f(l2 * (float)plan.seg_len);
+  const float l2 = log2_decay(plan.decay[h]);
+  const float all = decay_pow(l2, (float)plan.seg_len);
   const int i = blockIdx.y / Sh::kNW, j = blockIdx.y % Sh::kNW;
   f32x4 s{0.f, 0.f, 0.f, 0.f};
   if (role.first) {
-    const int r = St::row(i), c = in % plan.slices * VS + Sh::column(threadIdx.x & 15, St::tile(j));
+    const int r = St::row(i), c = (int)(in % plan.slices) * VS + Sh::column(threadIdx.x & 15, St::tile(j));
     const float* p = role.first + bh * role.dk * role.dv;
     if (r < role.dk && c < role.dv) {
       if (role.flip) s = *reinterpret_cast<const f32x4*>(p + (int64_t)c * role.dk + r);
@@ -596,8 +653,8 @@ __global__ __launch_bounds__(kThreads) void linattn_step_kernel(Strided q, Strid
                                                                 const int64_t* __restrict__ slots) {
   constexpr int RPB = kThreads / LPR;  // rows side by side
   __shared__ f32x4 part[kThreads / 64][LPR];
-  const int64_t b = blockIdx.x / H;
-  const int h = blockIdx.x - (int)b * H;
+  const int64_t b = blockIdx.x / (unsigned)H;
+  const int h = (int)(blockIdx.x % (unsigned)H);
   const int64_t slot = slots ? slots[b] : b;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c = (threadIdx.x & (LPR - 1)) * 4, r0 = threadIdx.x / LPR;
@@ -659,7 +716,10 @@ __global__ __launch_bounds__(kThreads) void linattn_step_kernel(Strided q, Strid
 }
 
 bool head_ok(int32_t w) { return w >= 8 && w <= 128 && w % 8 == 0; }
-bool strided_ok(const Strided& s) { return s.p && aligned16(s.p) && s.ts % 8 == 0 && s.hs % 8 == 0; }
+// (64 rows' offsets fit 32 bits)
+bool strided_ok(const Strided& s) {
+  return s.p && aligned16(s.p) && s.ts % 8 == 0 && s.hs % 8 == 0 && s.ts >= 0 && s.ts < (1 << 22);
+}
 bool state_ok(const float* p) { return aligned16(p); }
 
 // the block counts stay below 2^31 (kWantGroups and six per unit)
@@ -760,11 +820,11 @@ int launch(const Role* roles, int count, int32_t dtype, const int64_t* offsets, 
   p.offsets = offsets;
   p.decay = decay;
   p.blobs = static_cast<float*>(ws);
-  p.units = B * H;
-  p.H = H;
-  p.slices = (int)ceil_div(roles[0].dv, slice_width(roles[0].dv));
+  p.units = (unsigned)(B * H);
+  p.H = (unsigned)H;
+  p.slices = (unsigned)ceil_div(roles[0].dv, slice_width(roles[0].dv));
   p.inner = p.slices * count;
-  cut(p.units * p.inner, max_len, &p.segments, &p.seg_len);
+  cut((int64_t)p.units * p.inner, max_len, &p.segments, &p.seg_len);
   for (int i = 0; i < count; ++i) p.roles.r[i] = roles[i];
   return dtype == DLRM_F32 ? launch_type<float>(p, stream) : launch_type<uint16_t>(p, stream);
 }
