@@ -115,6 +115,10 @@ struct Mat<uint16_t> {
   static __device__ __forceinline__ void put4(uint16_t* p, f32x4 v) {
     *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
   }
+  // not 0 if an element of the word is not finite: its exponent's carry
+  static __device__ __forceinline__ uint32_t carry(uint32_t w) {
+    return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+  }
   // bit e: element e of 16 bytes is not finite
   static __device__ __forceinline__ uint32_t bad(uint4 u) {
     const uint32_t q[4] = {u.x, u.y, u.z, u.w};
@@ -161,6 +165,7 @@ struct Mat<float> {
     for (int n = 0; n < N; ++n) c[n] = mma(x, b[n], c[n]);
   }
   static __device__ __forceinline__ void put4(float* p, f32x4 v) { *reinterpret_cast<f32x4*>(p) = v; }
+  static __device__ __forceinline__ uint32_t carry(uint32_t w) { return ((w & 0x7f800000u) + 0x00800000u) & 0x80000000u; }
   static __device__ __forceinline__ uint32_t bad(uint4 u) {
     const uint32_t q[4] = {u.x, u.y, u.z, u.w};
     uint32_t m = 0;
@@ -202,7 +207,7 @@ struct Shape {
   static constexpr int kPS = VS + 4;
   static_assert(DK * kPS * 4 <= kTileBytes, "a state fits the tiles' LDS");
   // waves per SIMD that the LDS of whole workgroups leaves room for
-  static constexpr int kWaves = kBytes > 80 * 1024 ? 1 : kBytes > 53 * 1024 ? 2 : kBytes > 40 * 1024 ? 3 : 4;
+  static constexpr int kWaves = kBytes > 80 * 1024 ? 1 : kBytes > 53 * 1024 ? 2 : kBytes > 40 * 1024 || sizeof(T) == 4 ? 3 : 4;
   static constexpr int kBlob = kMW * kNW * 4;  // state floats per thread
   // column of the slice that index m of tile j stands for: a lane's tiles
   // then hold VS / 4 consecutive columns of a row of the output
@@ -380,23 +385,35 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(Shape<
   const uint32_t voff = (uint32_t)((back ? kC - VR * (VN - 1) - 1 - vr : vr) * (int)role.v.ts + col0 + vc) * sizeof(T);
   const uint32_t qoff = (uint32_t)(place(16 * wave + n) * (int)role.q.ts + g * (M::kWide / 4)) * sizeof(T);
   const uint32_t ooff = (uint32_t)(place(16 * wave + n) * (int)role.o.ts + col0 + (VS / 4) * g) * sizeof(T);
+  const bool full_width = dk == DK && col0 + VS <= dv;
   uint4 kreg[KN], vreg[VN];
   auto fetch = [&](int64_t c0) {
     const int empty = s1 - c0 < kC ? kC - (int)(s1 - c0) : 0;
     const char* k0 = window(role.k, c0 - empty);
     const char* v0 = window(role.v, c0 - empty);
     const uint32_t ko = local_copy(koff), vo = local_copy(voff);
+    auto k_at = [&](int i) {
+      return *reinterpret_cast<const uint4*>(k0 + (back ? KN - 1 - i : i) * KR * role.k.ts * (int64_t)sizeof(T) + ko);
+    };
+    auto v_at = [&](int i) {
+      return *reinterpret_cast<const uint4*>(v0 + (back ? VN - 1 - i : i) * VR * role.v.ts * (int64_t)sizeof(T) + vo);
+    };
+    if (full_width && empty == 0) {
+#pragma unroll
+      for (int i = 0; i < KN; ++i) kreg[i] = k_at(i);
+#pragma unroll
+      for (int i = 0; i < VN; ++i) vreg[i] = v_at(i);
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < KN; ++i) {
       kreg[i] = make_uint4(0u, 0u, 0u, 0u);
-      const int64_t step = (back ? KN - 1 - i : i) * KR * role.k.ts * (int64_t)sizeof(T);
-      if (kr + i * KR >= empty && kc < dk) kreg[i] = *reinterpret_cast<const uint4*>(k0 + step + ko);
+      if (kr + i * KR >= empty && kc < dk) kreg[i] = k_at(i);
     }
 #pragma unroll
     for (int i = 0; i < VN; ++i) {
       vreg[i] = make_uint4(0u, 0u, 0u, 0u);
-      const int64_t step = (back ? VN - 1 - i : i) * VR * role.v.ts * (int64_t)sizeof(T);
-      if (vr + i * VR >= empty && col0 + vc < dv) vreg[i] = *reinterpret_cast<const uint4*>(v0 + step + vo);
+      if (vr + i * VR >= empty && col0 + vc < dv) vreg[i] = v_at(i);
     }
   };
   constexpr int QN = DK / M::kWide;
@@ -405,6 +422,11 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(Shape<
     const int empty = s1 - c0 < kC ? kC - (int)(s1 - c0) : 0;
     const char* q0 = window(role.q, c0 - empty);
     const uint32_t qo = local_copy(qoff);
+    if (full_width && empty == 0) {
+#pragma unroll
+      for (int f = 0; f < QN; ++f) qf[f] = *reinterpret_cast<const Frag*>(q0 + f * M::kWide * sizeof(T) + qo);
+      return;
+    }
 #pragma unroll
     for (int f = 0; f < QN; ++f) {
       qf[f] = M::zero();
@@ -426,9 +448,10 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(Shape<
 
   // decays towards a chunk's end, of the last 16 places; an earlier tile's
   // are these times decay^16 per tile
-  const float l2 = log2_decay(plan.decay[h]);
-  const float kscale = role.kscale;
-  const float d16 = decay_pow(l2, 16.f);
+  auto uniform = [](float x) { return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(x))); };
+  const float l2 = uniform(log2_decay(plan.decay[h]));
+  const float d1 = uniform(decay_pow(l2, 1.f)), d16 = uniform(decay_pow(l2, 16.f));
+  const float kscale = role.kscale, oscale = role.oscale;
   f32x4 to_end;
 #pragma unroll
   for (int r = 0; r < 4; ++r) to_end[r] = kscale * decay_pow(l2, (float)(16 - lead - 4 * g - r));
@@ -449,7 +472,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(Shape<
       uint2* p = reinterpret_cast<uint2*>(Vs + e / VP * PV + e % VP * E);
       p[0] = make_uint2(vreg[i].x, vreg[i].y);
       p[1] = make_uint2(vreg[i].z, vreg[i].w);
-      bad |= M::bad(vreg[i]);
+      bad |= M::carry(vreg[i].x) | M::carry(vreg[i].y) | M::carry(vreg[i].z) | M::carry(vreg[i].w);
     }
     if (!ONLY_STATE) {
 #pragma unroll
@@ -485,13 +508,16 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(Shape<
 
     f32x4 out[NT];
     Frag pf[4 / M::kTiles];
-    // per-chunk copies: what is made from them is made again in each chunk,
-    // for kept outside the loop it would cost registers
-    const float tile_decay = local_copy(d16), l = local_copy(l2), lag = local_copy((float)(n - 4 * g));
+    // made from copies in each chunk: kept outside the loop, the weights would
+    // cost registers
+    const float tile_decay = local_copy(d16), lag = local_copy((float)(n - 4 * g));
     if (!ONLY_STATE) {
       // the masked, decayed products of this wave's 16 rows with the chunk's
       f32x4 p[4];
-      float far = 1.f;
+      f32x4 w;  // of the tile before the diagonal, then of the ones before that
+      w[3] = kscale * oscale * decay_pow(l2, lag + 13.f);
+#pragma unroll
+      for (int r = 2; r >= 0; --r) w[r] = w[r + 1] * d1;
 #pragma unroll
       for (int i = 3; i >= 0; --i) {
         p[i] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -502,11 +528,10 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(Shape<
           // selected, not multiplied: a masked product may not be finite
 #pragma unroll
           for (int r = 0; r < 4; ++r)
-            p[i][r] = lag >= (float)r ? p[i][r] * (kscale * decay_pow(l, lag - (float)r)) : 0.f;
+            p[i][r] = lag >= (float)r ? p[i][r] * (kscale * oscale * decay_pow(l2, lag - (float)r)) : 0.f;
         } else {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) p[i][r] *= kscale * decay_pow(l, lag + (float)(16 - r)) * far;
-          far *= tile_decay;
+          p[i] *= w;
+          w *= tile_decay;
         }
       }
 #pragma unroll
@@ -518,7 +543,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(Shape<
 #pragma unroll
         for (int j = 0; j < NT; ++j) out[j] = M::mma(M::wide(Ss + (16 * j + n) * PK + f * M::kWide, g), qf[f], out[j]);
       // (an empty place's power may be any; its row is not stored)
-      const float from_state = decay_pow(l, (float)(16 * wave + n - (kC - m) + lead));
+      const float from_state = oscale * decay_pow(l2, local_copy((float)n) + (float)(16 * wave - (kC - m) + lead));
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -538,7 +563,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(Shape<
         char* row = const_cast<char*>(window(role.o, c0 - (kC - m))) + local_copy(ooff);
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-          f32x4 o = out[j] * role.oscale;
+          f32x4 o = out[j];
           if (any_bad) {
             const int cold = local_copy(lane);
 #pragma unroll
