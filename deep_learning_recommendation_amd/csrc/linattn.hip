@@ -618,12 +618,11 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(Shape<
 
 // The states that enter the segments, in place of those that the segments
 // made from zero: in[s] = decay^seg_len in[s - 1] + made[s - 1].  A thread
-// takes four elements along the segments, kAhead loads in flight.
-constexpr int kAhead = 16;
+// takes one element along the segments, kAhead loads in flight.
+constexpr int kAhead = 64;
 template <class T, int DK, int VS>
 __global__ __launch_bounds__(kThreads) void linattn_scan_kernel(Plan plan) {
   using Sh = Shape<T, DK, VS>;
-  using St = State<T, DK, VS>;
   constexpr int64_t kBlobFloats = (int64_t)Sh::kBlob * kThreads;
   unsigned unit, in;
   if (!locate(plan, plan.units, &unit, &in)) return;
@@ -634,23 +633,18 @@ __global__ __launch_bounds__(kThreads) void linattn_scan_kernel(Plan plan) {
   const int used = len > 0 ? (int)((len + plan.seg_len - 1) / plan.seg_len) : 1;  // segments that have rows
   const float l2 = log2_decay(plan.decay[h]);
   const float all = decay_pow(l2, (float)plan.seg_len);
-  const int i = blockIdx.y / Sh::kNW, j = blockIdx.y % Sh::kNW;
-  f32x4 s{0.f, 0.f, 0.f, 0.f};
-  if (role.first) {
-    const int r = St::row(i), c = (int)(in % plan.slices) * VS + Sh::column(threadIdx.x & 15, St::tile(j));
-    const float* p = role.first + bh * role.dk * role.dv;
-    if (r < role.dk && c < role.dv) {
-      if (role.flip) s = *reinterpret_cast<const f32x4*>(p + (int64_t)c * role.dk + r);
-      else
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[e] = p[(r + e) * role.dv + c];
-    }
-  }
-  const int64_t pitch = plan.inner * kBlobFloats / 4;
-  f32x4* p = reinterpret_cast<f32x4*>(plan.blobs + (bh * plan.segments * plan.inner + in) * kBlobFloats) +
-             (int64_t)blockIdx.y * kThreads + threadIdx.x;
+  // the element's place in the blob (tile, thread, element) and in the state
+  const int at = blockIdx.y * kThreads + threadIdx.x;
+  const int tile = at / (4 * kThreads), t = at / 4 % kThreads, lane = t & 63, wave = t >> 6;
+  const int r = 16 * ((wave % Sh::kWM) * Sh::kMW + tile / Sh::kNW) + 4 * (lane >> 4) + (at & 3);
+  const int c = (int)(in % plan.slices) * VS + Sh::column(lane & 15, wave / Sh::kWM * Sh::kNW + tile % Sh::kNW);
+  float s = 0.f;
+  if (role.first && r < role.dk && c < role.dv)
+    s = role.first[bh * role.dk * role.dv + (role.flip ? c * role.dk + r : r * role.dv + c)];
+  const int64_t pitch = plan.inner * kBlobFloats;
+  float* p = plan.blobs + (bh * plan.segments * plan.inner + in) * kBlobFloats + at;
   for (int s0 = 0; s0 < used; s0 += kAhead) {
-    f32x4 made[kAhead];
+    float made[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u)
       if (s0 + u + 1 < used) made[u] = p[(s0 + u) * pitch];
@@ -658,10 +652,7 @@ __global__ __launch_bounds__(kThreads) void linattn_scan_kernel(Plan plan) {
     for (int u = 0; u < kAhead; ++u) {
       if (s0 + u >= used) break;
       p[(s0 + u) * pitch] = s;
-      if (s0 + u + 1 < used) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[e] = s[e] * all + made[u][e];
-      }
+      if (s0 + u + 1 < used) s = s * all + made[u];
     }
   }
 }
@@ -817,7 +808,7 @@ int launch_shape(const Plan& plan, hipStream_t stream) {
     hipLaunchKernelGGL((linattn_kernel<T, DK, VS, true>), blocks(plan.units * (plan.segments - 1)), dim3(kThreads), lds,
                        stream, plan);
     dim3 scan = blocks(plan.units);
-    scan.y = Shape<T, DK, VS>::kBlob / 4;
+    scan.y = Shape<T, DK, VS>::kBlob;
     hipLaunchKernelGGL((linattn_scan_kernel<T, DK, VS>), scan, dim3(kThreads), 0, stream, plan);
   }
   hipLaunchKernelGGL((linattn_kernel<T, DK, VS, false>), blocks(plan.units * plan.segments), dim3(kThreads), lds, stream,
