@@ -757,12 +757,17 @@ int pad_width(int32_t w) { return w <= 32 ? 32 : w <= 64 ? 64 : 128; }
 int slice_width(int32_t w) { return w <= 32 ? 32 : 64; }
 
 // Segments of a launch: enough workgroups for the device from few long
-// histories, none shorter than kSegMin rows.
-constexpr int64_t kSegMin = 256;
-constexpr int64_t kWantGroups = 1024;
-void cut(int64_t groups, int64_t max_len, int* segments, int64_t* seg_len) {
+// histories, none so short that the state of a segment (made, joined and read
+// again: 4 reads and writes of DK x VS floats) costs more than its rows.
+// Measured, histories x rows x heads x width, with 1024 workgroups of at least
+// 256 rows and with 2048 of at least 2 DK: 16 x 2500 x 4 x 64 54 -> 45 us,
+// 2 x 1500 x 2 x 64 27 -> 20 us, 1 x 1000 x 2 x 64 29 -> 19 us, gradient of
+// 4 x 5000 x 4 x 128 182 -> 140 us; at 128 rows and width 128, 1 x 20011 x 4
+// takes 72 us instead of 60.
+constexpr int64_t kWantGroups = 2048;
+void cut(int64_t groups, int64_t max_len, int dk, int* segments, int64_t* seg_len) {
   int64_t want = groups > 0 ? kWantGroups / groups : 1;
-  const int64_t most = max_len / kSegMin;
+  const int64_t most = max_len / (2 * dk);
   want = want < most ? want : most;
   if (want < 2) {
     *segments = 1;
@@ -778,7 +783,7 @@ size_t blob_bytes(int64_t units, int count, int64_t max_len, int32_t dk, int32_t
   const int vs = slice_width(dv), slices = (int)ceil_div(dv, vs);
   int segments;
   int64_t seg_len;
-  cut(units * slices * count, max_len, &segments, &seg_len);
+  cut(units * slices * count, max_len, pad_width(dk), &segments, &seg_len);
   if (segments < 2) return 0;
   return (size_t)units * segments * slices * count * pad_width(dk) * vs * 4;
 }
@@ -840,7 +845,7 @@ int launch(const Role* roles, int count, int32_t dtype, const int64_t* offsets, 
   p.H = (unsigned)H;
   p.slices = (unsigned)ceil_div(roles[0].dv, slice_width(roles[0].dv));
   p.inner = p.slices * count;
-  cut((int64_t)p.units * p.inner, max_len, &p.segments, &p.seg_len);
+  cut((int64_t)p.units * p.inner, max_len, pad_width(roles[0].dk), &p.segments, &p.seg_len);
   for (int i = 0; i < count; ++i) p.roles.r[i] = roles[i];
   return dtype == DLRM_F32 ? launch_type<float>(p, stream) : launch_type<uint16_t>(p, stream);
 }
