@@ -289,9 +289,17 @@ def _addr(t) -> int | None:
 
 
 def _raw_stream(stream) -> int:
+    """The hipStream_t of a torch stream, or of the current one: its handle
+    straight from torch's C module where that is there (the stream object
+    that torch.cuda.current_stream() makes costs 3 us, as much as a launch)."""
+    if stream is not None:
+        return stream.cuda_stream
     import torch
 
-    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+    handle = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if handle is None:
+        return torch.cuda.current_stream().cuda_stream
+    return handle(torch.cuda.current_device())
 
 
 def _bytes(ws) -> int:

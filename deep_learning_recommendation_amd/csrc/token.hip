@@ -44,26 +44,27 @@ __global__ __launch_bounds__(256) void token_fwd_kernel(const TI* __restrict__ t
   const int64_t groups = 256 >> g_log2;
   const int64_t i0 = ((int64_t)blockIdx.x * groups + (threadIdx.x >> g_log2)) * kRows;
   if (i0 >= n) return;
+  // a token that names no row reads row 0 and writes zeros: no branch splits
+  // the batch of loads
   int64_t t[kRows];
+  bool named[kRows];
 #pragma unroll
-  for (int j = 0; j < kRows; ++j) t[j] = i0 + j < n ? tokens[i0 + j] : -1;
+  for (int j = 0; j < kRows; ++j) {
+    t[j] = tokens[i0 + j < n ? i0 + j : n - 1];
+    named[j] = t[j] >= 0 && t[j] < rows;
+    t[j] = named[j] ? t[j] : 0;
+  }
   for (int col = gl * VE; col < d; col += GL * VE) {
     Piece<TI, VE> in[kRows];
 #pragma unroll
-    for (int j = 0; j < kRows; ++j)
-      if (t[j] >= 0 && t[j] < rows) in[j].load(table + t[j] * d + col);
+    for (int j = 0; j < kRows; ++j) in[j].load(table + t[j] * d + col);
 #pragma unroll
     for (int j = 0; j < kRows; ++j) {
-      if (i0 + j >= n) continue;
+      if (i0 + j >= n) break;
       float v[VE];
-      if (t[j] >= 0 && t[j] < rows) {
-        in[j].get(v);
+      in[j].get(v);
 #pragma unroll
-        for (int c = 0; c < VE; ++c) v[c] *= scale;
-      } else {
-#pragma unroll
-        for (int c = 0; c < VE; ++c) v[c] = 0.f;
-      }
+      for (int c = 0; c < VE; ++c) v[c] = named[j] ? v[c] * scale : 0.f;
       Piece<TO, VE> o;
       o.set(v);
       o.store(out + (i0 + j) * out_ld + col);
@@ -267,28 +268,31 @@ __global__ __launch_bounds__(256) void token_chunk_kernel(const uint32_t* __rest
     else if (on) put_row<VE>(dtable + (int64_t)cur * d + col, acc, scale, add);
   };
   if (live) {
+    const int from = on ? col : 0;  // every lane loads, every position has a row: no branch splits the batch
     for (int q0 = 0; q0 < chunk_len; q0 += kBatch) {
       Piece<T, VE> in[kBatch];
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u)
-        if (on && ck[q0 + u] < rows) in[u].load(dout + (int64_t)cp[q0 + u] * ld + col);
+      uint32_t pos[kBatch], key[kBatch];
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
-        const uint32_t key = ck[q0 + u];
-        if (key >= rows) break;
-        if (key != cur) {
+        pos[u] = cp[q0 + u];
+        key[u] = ck[q0 + u];
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) in[u].load(dout + (int64_t)pos[u] * ld + from);
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        if (key[u] >= rows) break;
+        if (key[u] != cur) {
           close();
-          cur = key;
+          cur = key[u];
           open = false;
 #pragma unroll
           for (int c = 0; c < VE; ++c) acc[c] = 0.f;
         }
-        if (on) {
-          float v[VE];
-          in[u].get(v);
+        float v[VE];
+        in[u].get(v);
 #pragma unroll
-          for (int c = 0; c < VE; ++c) acc[c] += v[c];
-        }
+        for (int c = 0; c < VE; ++c) acc[c] += v[c];
       }
     }
   }
@@ -340,9 +344,9 @@ __device__ __forceinline__ void add_partials(const float* __restrict__ head, con
   for (int64_t i0 = first; i0 <= m; i0 += step * kJoinFlight) {
     Piece<float, VE> p[kJoinFlight];
 #pragma unroll
-    for (int u = 0; u < kJoinFlight; ++u) {
-      const int64_t i = i0 + u * step;
-      if (i <= m) p[u].load((i == 0 ? tail + block * d : head + (block + i) * d) + col);
+    for (int u = 0; u < kJoinFlight; ++u) {  // past the run's end: its last partial again, not added
+      const int64_t i = i0 + u * step <= m ? i0 + u * step : m;
+      p[u].load((i == 0 ? tail + block * d : head + (block + i) * d) + col);
     }
 #pragma unroll
     for (int u = 0; u < kJoinFlight; ++u) {
