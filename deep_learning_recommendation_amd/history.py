@@ -1,0 +1,235 @@
+"""A tower that turns a user's behaviour history into one vector.
+
+A history is a ragged list of item tokens, the newest last.  Its vector has
+the width d of the embedding tables: it can stand as one more row of X for the
+interaction, or be stored as an int8 table row that the low-precision lookup
+reads.  The tower holds device buffers (torch tensors: memory only) and orders
+calls of the library; it performs no arithmetic itself.
+
+    x    = sqrt(d) * T[token]                      dlrm_token_embed_fwd
+    for each layer, the residual stream h (at first none):
+      h, y = h + dropout(x), rms_norm(h) * w       dlrm_add_rmsnorm_fwd
+      q,k,v = y Wqkv^T                             dlrm_linear_fwd / dlrm_mlp_fwd
+      o    = linear attention with a decay per head dlrm_linattn_fwd
+      x    = o Wo^T                                dlrm_linear_fwd / dlrm_mlp_fwd
+    y    = rms_norm(h + dropout(x)) * w_out        dlrm_add_rmsnorm_fwd
+    out  = y of each history's newest event        dlrm_token_embed_fwd on y
+
+Serving (``train=False``) keeps activations in bf16, has no dropout and two
+forms: ``forward`` over whole histories, which also leaves every layer's
+attention states, and ``step``, one new event per user on pools of states.
+Training (``train=True``) keeps activations in fp32 around the bf16 MFMA
+GEMMs of ``dlrm_mlp_fwd`` / ``dlrm_mlp_bwd``, and ``backward`` returns the
+gradient of every parameter.
+"""
+from __future__ import annotations
+
+import math
+from dataclasses import dataclass
+
+import torch
+
+from . import _lib as C
+from .pipeline import MLPParams, make_mlp
+
+
+@dataclass
+class HistoryLayer:
+    w: torch.Tensor       # fp32 [d], the norm's weights
+    qkv: MLPParams        # d -> H (2 dk + dv)
+    out: MLPParams        # H dv -> d
+    decay: torch.Tensor   # fp32 [H]
+
+
+def make_layer(w, Wqkv, Wo, decay, device="cuda") -> HistoryLayer:
+    """Device parameters from host arrays (projections without biases)."""
+    zeros = lambda W: torch.zeros(W.shape[0])  # noqa: E731
+    f32 = lambda t: torch.as_tensor(t, dtype=torch.float32).to(device).contiguous()  # noqa: E731
+    return HistoryLayer(f32(w), make_mlp((Wqkv.shape[1], Wqkv.shape[0]), [Wqkv], [zeros(Wqkv)], True, device),
+                        make_mlp((Wo.shape[1], Wo.shape[0]), [Wo], [zeros(Wo)], True, device), f32(decay))
+
+
+class HistoryTower:
+    """Parameters and call sequence; buffers are made per batch shape."""
+
+    def __init__(self, table, layers, w_out, H: int, dk: int, dv: int, eps: float = 1e-6, train: bool = False,
+                 p: float = 0.0):
+        """table: bf16 or fp32 [V][d]; layers: HistoryLayer list; p: dropout on
+        every residual branch (training only)."""
+        self.table, self.layers, self.w_out = table, list(layers), w_out
+        self.V, self.d = table.shape
+        self.H, self.dk, self.dv, self.eps = H, dk, dv, eps
+        self.train, self.p = train, p if train else 0.0
+        if p and not train:
+            raise ValueError("dropout needs train=True")
+        for lay in self.layers:
+            if lay.qkv.dims != (self.d, H * (2 * dk + dv)) or lay.out.dims != (H * dv, self.d):
+                raise ValueError("a layer's projections do not fit d, H, dk and dv")
+        self.act = torch.float32 if train else torch.bfloat16
+        self.scale = dk ** -0.5
+        dev = table.device
+        # (seed, offset) of the branches' dropout; the offset moves on the
+        # device, so that a replayed graph draws new masks
+        self.rng = torch.zeros((len(self.layers) + 1, 2), dtype=torch.int64, device=dev)
+        self.states = None  # per layer, after forward(): fp32 [B][H][dk][dv]
+
+    def seed(self, seed: int) -> None:
+        """New dropout streams, one per branch."""
+        for i in range(self.rng.shape[0]):
+            self.rng[i, 0], self.rng[i, 1] = seed * (self.rng.shape[0] + 1) + i, 0
+
+    def _empty(self, *shape, dtype=None):
+        return torch.empty(shape, dtype=dtype or self.act, device=self.table.device)
+
+    def _ws(self, nbytes: int):
+        return self._empty(max(nbytes, 256), dtype=torch.uint8)
+
+    def _linear(self, x, mlp: MLPParams, n: int, keep, stream):
+        """x [n][in] times a projection; in training the call that the backward
+        pass continues (its workspace goes to ``keep``)."""
+        k, m = mlp.dims
+        y = self._empty(n, m)
+        if self.train:
+            ws = self._ws(C.dlrm_mlp_workspace_size(n, mlp.dims, mlp.w_dtype, True))
+            C.dlrm_mlp_fwd(x, k, n, mlp.dims, mlp.Ws, mlp.w_ld, mlp.biases, mlp.w_dtype, C.DLRM_ACT_NONE, y, m, None,
+                           ws, True, stream)
+            keep.append((ws, y))
+        else:
+            C.dlrm_linear_fwd(x, k, mlp.Ws[0], mlp.w_ld[0], None, y, m, n, m, k, C.DLRM_ACT_NONE, stream)
+        return y
+
+    def _heads(self, qkv):
+        """q, k, v views of a projection's output rows."""
+        H, dk, dv = self.H, self.dk, self.dv
+        return (qkv[:, :H * dk].unflatten(1, (H, dk)), qkv[:, H * dk:2 * H * dk].unflatten(1, (H, dk)),
+                qkv[:, 2 * H * dk:].unflatten(1, (H, dv)))
+
+    def _norm(self, i, x, res, w, n, stream, y=None, scale_bias=None):
+        h = self._empty(n, self.d)
+        y = self._empty(n, self.d) if y is None else y
+        rstd = self._empty(n, dtype=torch.float32)
+        C.dlrm_add_rmsnorm_fwd(x, self.d, res, self.d, w, n, self.d, self.eps, self.p, self.rng[i], h, self.d, y, self.d,
+                               scale_bias, rstd, stream)
+        return h, y, rstd
+
+    def _events(self, tokens, attend, stream, rows=None):
+        """The layers over n events; attend(layer number, q, k, v, o).  Returns
+        the last norm's output, or int8 rows in ``rows`` = (y, scale_bias)."""
+        n, d = tokens.numel(), self.d
+        x = self._empty(n, d)
+        C.dlrm_token_embed_fwd(self.table, self.V, d, tokens, n, math.sqrt(d), x, d, stream)
+        res, self._saved = None, []
+        for i, lay in enumerate(self.layers):
+            keep = []
+            h, y, rstd = self._norm(i, x, res, lay.w, n, stream)
+            qkv = self._linear(y, lay.qkv, n, keep, stream)
+            o = self._empty(n, self.H, self.dv)
+            attend(i, *self._heads(qkv), o)
+            x, res = self._linear(o.view(n, -1), lay.out, n, keep, stream), h
+            if self.train:
+                self._saved.append((h, rstd, qkv, o, keep))
+        y, sb = rows if rows is not None else (None, None)
+        h, y, rstd = self._norm(len(self.layers), x, res, self.w_out, n, stream, y, sb)
+        if self.train:
+            self._saved.append((h, rstd))
+        return y
+
+    def forward(self, tokens, offsets, max_len: int, out, out_ld: int, stream=None):
+        """Whole histories: tokens int64 [n], offsets int64 [B + 1] from 0, none
+        longer than max_len.  Writes each history's vector (zeros for an empty
+        one) to fp32 rows of ``out``, leaves the attention states in
+        ``self.states``."""
+        B, n = offsets.numel() - 1, tokens.numel()
+        if n == 0:  # every history is empty: zeros, from a lookup that names no row
+            if self.train:
+                raise ValueError("a training batch without events")
+            self.states = [self._empty(B, self.H, self.dk, self.dv, dtype=torch.float32).zero_() for _ in self.layers]
+            nobody = torch.full((B,), -1, dtype=torch.int64, device=self.table.device)
+            C.dlrm_token_embed_fwd(self.table, self.V, self.d, nobody, B, 1.0, out, out_ld, stream)
+            return out
+        self.states = [self._empty(B, self.H, self.dk, self.dv, dtype=torch.float32) for _ in self.layers]
+        shape = (B, self.H, max_len, self.dk, self.dv)
+        ws = self._ws(C.dlrm_linattn_workspace_size(*shape))
+
+        def attend(i, q, k, v, o):
+            C.dlrm_linattn_fwd(q, k, v, offsets, *shape, self.layers[i].decay, self.scale, None, o, self.states[i], ws,
+                               stream)
+
+        y = self._events(tokens, attend, stream)
+        last = torch.where(offsets[1:] > offsets[:-1], offsets[1:] - 1, -1)
+        C.dlrm_token_embed_fwd(y, n, self.d, last, B, 1.0, out, out_ld, stream)
+        if self.train:
+            self._batch = (tokens, offsets, max_len, last)
+        return out
+
+    def step(self, tokens, pools, slots, out=None, out_ld: int = 0, rows=None, stream=None):
+        """One new event per user: tokens int64 [B], pools the layers' states
+        fp32 [pool][H][dk][dv], slots int64 [B] (or None) the users' entries
+        (distinct; -1: no user).  Writes the users' vectors to ``out`` (fp32
+        rows), or with ``rows`` = (int8 [B][d], fp32 [B][2]) as int8 table rows
+        and their scales and biases, which dlrm_embbag_fwd_lp reads."""
+        if self.train:
+            raise ValueError("step() is a serving call")
+        B = tokens.numel()
+
+        def attend(i, q, k, v, o):
+            C.dlrm_linattn_step(q, k, v, B, self.H, self.dk, self.dv, self.layers[i].decay, self.scale, pools[i], slots,
+                                o, stream)
+
+        y = self._events(tokens, attend, stream, rows)
+        if rows is None:
+            every = torch.arange(B, device=tokens.device)
+            C.dlrm_token_embed_fwd(y, B, self.d, every, B, 1.0, out, out_ld, stream)
+            return out
+        return rows
+
+    def backward(self, dout, dout_ld: int, stream=None) -> dict:
+        """Gradients of the last ``forward`` (train=True) from those of its fp32
+        output rows: {"table" fp32 [V][d], "w_out", "layers": [{"w", "qkv",
+        "out"}]}.  Moves the dropout's offsets on, so the next forward draws
+        new masks."""
+        if not self.train:
+            raise ValueError("backward() needs train=True")
+        tokens, offsets, max_len, last = self._batch
+        n, B, d, H, dk, dv = tokens.numel(), last.numel(), self.d, self.H, self.dk, self.dv
+        f32 = dict(dtype=torch.float32)
+
+        def embed_bwd(tok, count, g, ld, rows, scale):
+            dT = self._empty(rows, d, **f32)
+            ws = self._ws(C.dlrm_token_embed_bwd_workspace_size(count, rows, d))
+            C.dlrm_token_embed_bwd(tok, count, g, ld, rows, d, scale, dT, False, ws, stream)
+            return dT
+
+        def norm_bwd(i, dy, dh, h, rstd, w):
+            dx, dres, dw = self._empty(n, d), self._empty(n, d), self._empty(d, **f32)
+            ws = self._ws(C.dlrm_add_rmsnorm_bwd_workspace_size(n, d))
+            C.dlrm_add_rmsnorm_bwd(dy, d, dh, d, h, d, w, rstd, n, d, self.p, self.rng[i], dx, d, dres, d, dw, ws,
+                                   stream)
+            return dx, dres, dw
+
+        def linear_bwd(mlp, kept, g):
+            k, m = mlp.dims
+            dW, db, dx = self._empty(m, k, **f32), self._empty(m, **f32), self._empty(n, k, **f32)
+            ws = self._ws(C.dlrm_mlp_bwd_workspace_size(n, mlp.dims))
+            C.dlrm_mlp_bwd(n, mlp.dims, mlp.Ws, mlp.w_ld, C.DLRM_ACT_NONE, kept[0], kept[1], m, g, m, [dW], [db], dx, k,
+                           ws, stream)
+            return dx, dW
+
+        dy = embed_bwd(last, B, dout, dout_ld, n, 1.0)
+        h, rstd = self._saved[-1]
+        dx, dres, dw = norm_bwd(len(self.layers), dy, None, h, rstd, self.w_out)
+        grads = {"w_out": dw, "layers": []}
+        shape = (B, H, max_len, dk, dv)
+        ws = self._ws(C.dlrm_linattn_bwd_workspace_size(*shape))
+        for i in reversed(range(len(self.layers))):
+            lay, (h, rstd, qkv, _, kept) = self.layers[i], self._saved[i]
+            do, dWo = linear_bwd(lay.out, kept[1], dx)
+            dqkv = self._empty(n, qkv.shape[1])
+            C.dlrm_linattn_bwd(*self._heads(qkv), do.view(n, H, dv), offsets, *shape, lay.decay, self.scale, None, None,
+                               *self._heads(dqkv), None, ws, stream)
+            dy, dWqkv = linear_bwd(lay.qkv, kept[0], dqkv)
+            dx, dres, dw = norm_bwd(i, dy, dres, h, rstd, lay.w)
+            grads["layers"].insert(0, {"w": dw, "qkv": dWqkv, "out": dWo})
+        grads["table"] = embed_bwd(tokens, n, dx, d, self.V, math.sqrt(d))
+        self.rng[:, 1] += (n * d + 7) // 8
+        return grads
