@@ -112,6 +112,10 @@ struct Mat<uint16_t> {
       }
     }
   }
+  // kPiece elements of an output row
+  static __device__ __forceinline__ void put16(uint16_t* p, const f32x4* t) {
+    stream(reinterpret_cast<uint4*>(p), __builtin_bit_cast(uint4, pack(t)));
+  }
   static __device__ __forceinline__ void put4(uint16_t* p, f32x4 v) {
     *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
   }
@@ -163,6 +167,9 @@ struct Mat<float> {
     for (int r = 0; r < 4; ++r) x[r] = a[r] * w[0][r];
 #pragma unroll
     for (int n = 0; n < N; ++n) c[n] = mma(x, b[n], c[n]);
+  }
+  static __device__ __forceinline__ void put16(float* p, const f32x4* t) {
+    stream(reinterpret_cast<float4*>(p), __builtin_bit_cast(float4, t[0]));
   }
   static __device__ __forceinline__ void put4(float* p, f32x4 v) { *reinterpret_cast<f32x4*>(p) = v; }
   static __device__ __forceinline__ uint32_t carry(uint32_t w) { return ((w & 0x7f800000u) + 0x00800000u) & 0x80000000u; }
@@ -280,7 +287,8 @@ struct State {
     for (int e = threadIdx.x; e < DK * (VS / 4); e += kThreads) {
       const int r = e / (VS / 4), c = e % (VS / 4) * 4;
       if (r < dk && col0 + c < dv)
-        *reinterpret_cast<f32x4*>(p + r * dv + col0 + c) = *reinterpret_cast<const f32x4*>(lds + r * Sh::kPS + c);
+        __builtin_nontemporal_store(*reinterpret_cast<const f32x4*>(lds + r * Sh::kPS + c),
+                                    reinterpret_cast<f32x4*>(p + r * dv + col0 + c));
     }
   }
   // a segment's state in the workspace: 16 bytes per thread and tile
@@ -561,17 +569,17 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(Shape<
       }
       if (16 * wave + n >= kC - m) {
         char* row = const_cast<char*>(window(role.o, c0 - (kC - m))) + local_copy(ooff);
+        if (any_bad) {
+          const int cold = local_copy(lane);
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          f32x4 o = out[j];
-          if (any_bad) {
-            const int cold = local_copy(lane);
+          for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-              if (first_bad[(VS / 4) * (cold >> 4) + 4 * j + r] <= 16 * wave + (cold & 15)) o[r] += nan;
-          }
-          if (col0 + (VS / 4) * g + 4 * j < dv) M::put4(reinterpret_cast<T*>(row) + 4 * j, o);
+              if (first_bad[(VS / 4) * (cold >> 4) + 4 * j + r] <= 16 * wave + (cold & 15)) out[j][r] += nan;
         }
+#pragma unroll
+        for (int j = 0; j < NT; j += E / 4)  // 16 bytes at a time
+          if (col0 + (VS / 4) * g + 4 * j < dv) M::put16(reinterpret_cast<T*>(row) + 4 * j, out + j);
       }
     }
     // the state, after the output has left its registers

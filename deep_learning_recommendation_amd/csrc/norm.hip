@@ -65,6 +65,7 @@ struct Out<int8_t, VE> {
 #pragma unroll
       for (int j = 0; j < 4; ++j) w[i] |= ((uint32_t)(int)v[4 * i + j] & 0xffu) << (8 * j);
     }
+    // (kept in the caches: int8 rows are small, and read next by a lookup)
     if constexpr (VE == 8) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
     else *reinterpret_cast<uint32_t*>(p) = w[0];
   }
@@ -273,7 +274,9 @@ __global__ __launch_bounds__(kThreads) void addnorm_bwd_kernel(Bwd a) {
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       const int c = (i * LPR + G::lane()) * VE;
-      if (c < a.d) Out<float, VE>::store(part + c, dw[i]);
+      if (c < a.d)
+#pragma unroll
+        for (int j = 0; j < VE; ++j) part[c + j] = dw[i][j];
     }
   } else {
     __shared__ float s[kThreads / 64][LPR * NP * VE];

@@ -4,6 +4,7 @@
 #pragma once
 
 #include "common.hpp"
+#include "rows.hpp"
 
 namespace dlrm {
 namespace {
@@ -38,7 +39,7 @@ struct Clear {
   __device__ __forceinline__ void run() const {
     const int64_t blocks = (int64_t)(gridDim.x - first) * gridDim.y;
     const int64_t b = (int64_t)(blockIdx.x - first) * gridDim.y + blockIdx.y;
-    for (int64_t i = b * blockDim.x + threadIdx.x; i < n; i += blocks * blockDim.x) p[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int64_t i = b * blockDim.x + threadIdx.x; i < n; i += blocks * blockDim.x) stream(p + i, make_float4(0.f, 0.f, 0.f, 0.f));
   }
 };
 constexpr int kClearPerBlock = 256 * 16;  // float4s

@@ -13,6 +13,26 @@ inline bool rows_aligned(const void* p, int64_t ld, size_t elem, size_t bytes) {
   return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0 && (((size_t)ld * elem) & (bytes - 1)) == 0;
 }
 
+// Stores that pass the caches: an output is written once and is as large as
+// what the caches hold, or larger; kept there, it would only delay the inputs
+// behind it.  Measured: dropout of 819200 x 128 bf16 74 -> 58 us, residual +
+// norm of 131072 x 512 bf16 100 -> 83 us, clearing a 512 MB table gradient
+// before 819200 gradient rows are read 201 -> 158 us (whole call); the norm
+// followed by a call that reads its output is no slower at any size from 1 to
+// 512 MB (8 MB 11.5 -> 10.8 us, 512 MB 643 -> 612 us).
+typedef float stream_f4 __attribute__((ext_vector_type(4)));
+typedef uint32_t stream_u2 __attribute__((ext_vector_type(2)));
+typedef uint32_t stream_u4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ void stream(float4* p, float4 v) {
+  __builtin_nontemporal_store(stream_f4{v.x, v.y, v.z, v.w}, reinterpret_cast<stream_f4*>(p));
+}
+__device__ __forceinline__ void stream(uint2* p, uint2 v) {
+  __builtin_nontemporal_store(stream_u2{v.x, v.y}, reinterpret_cast<stream_u2*>(p));
+}
+__device__ __forceinline__ void stream(uint4* p, uint4 v) {
+  __builtin_nontemporal_store(stream_u4{v.x, v.y, v.z, v.w}, reinterpret_cast<stream_u4*>(p));
+}
+
 // VE elements of T as they lie in memory: 16 bytes, or 8 for four bf16.
 template <class T, int VE>
 struct Piece;
@@ -23,7 +43,7 @@ struct Piece<float, 4> {
   __device__ __forceinline__ void load(const float* p) { u = *reinterpret_cast<const float4*>(p); }
   __device__ __forceinline__ void get(float (&v)[4]) const { v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w; }
   __device__ __forceinline__ void set(const float (&v)[4]) { u = make_float4(v[0], v[1], v[2], v[3]); }
-  __device__ __forceinline__ void store(float* p) const { *reinterpret_cast<float4*>(p) = u; }
+  __device__ __forceinline__ void store(float* p) const { stream(reinterpret_cast<float4*>(p), u); }
 };
 template <>
 struct Piece<uint16_t, 4> {
@@ -36,7 +56,7 @@ struct Piece<uint16_t, 4> {
   __device__ __forceinline__ void set(const float (&v)[4]) {
     u = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
   }
-  __device__ __forceinline__ void store(uint16_t* p) const { *reinterpret_cast<uint2*>(p) = u; }
+  __device__ __forceinline__ void store(uint16_t* p) const { stream(reinterpret_cast<uint2*>(p), u); }
 };
 template <>
 struct Piece<float, 8> {
@@ -54,8 +74,8 @@ struct Piece<float, 8> {
     b = make_float4(v[4], v[5], v[6], v[7]);
   }
   __device__ __forceinline__ void store(float* p) const {
-    reinterpret_cast<float4*>(p)[0] = a;
-    reinterpret_cast<float4*>(p)[1] = b;
+    stream(reinterpret_cast<float4*>(p), a);
+    stream(reinterpret_cast<float4*>(p) + 1, b);
   }
 };
 template <>
@@ -72,7 +92,7 @@ struct Piece<uint16_t, 8> {
     u = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                    pack_bf16x2(v[6], v[7]));
   }
-  __device__ __forceinline__ void store(uint16_t* p) const { *reinterpret_cast<uint4*>(p) = u; }
+  __device__ __forceinline__ void store(uint16_t* p) const { stream(reinterpret_cast<uint4*>(p), u); }
 };
 
 __device__ __forceinline__ float to_f32(float x) { return x; }
