@@ -317,6 +317,7 @@ struct Plan {
   unsigned H, slices, inner;  // inner = slices * roles
   int segments;
   int64_t seg_len;  // rows per segment, a multiple of kC
+  const int32_t* order;  // nullable (one segment only): the histories, longest first
   Roles roles;
 };
 // The slices and roles of a unit read the same rows: they are eight blocks
@@ -354,10 +355,12 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(Shape<
   const unsigned segs = ONLY_STATE ? plan.segments - 1 : plan.segments;
   unsigned unit, in;
   if (!locate(plan, plan.units * segs, &unit, &in)) return;
-  const int64_t bh = unit / segs;
   const int seg = (int)(unit % segs);
-  const int64_t b = (unsigned)bh / plan.H;
-  const int h = (int)((unsigned)bh % plan.H);
+  unsigned history = unit / segs / plan.H;
+  if (plan.order) history = (unsigned)plan.order[history];
+  const int64_t b = history;
+  const int h = (int)(unit / segs % plan.H);
+  const int64_t bh = b * plan.H + h;
   const Role& role = plan.roles.r[in / plan.slices];
   const int col0 = (int)(in % plan.slices) * VS;
   const int64_t beg = plan.offsets[b], len = plan.offsets[b + 1] - beg;
@@ -665,6 +668,40 @@ __global__ __launch_bounds__(kThreads) void linattn_scan_kernel(Plan plan) {
   }
 }
 
+// The histories, longest first to within 1/256 of max_len, by counting (in
+// any order within a count: the order only says which workgroups start first,
+// no result depends on it).  One block.
+constexpr int kOrderThreads = 1024, kOrderBins = 256;
+__global__ __launch_bounds__(kOrderThreads) void linattn_order_kernel(const int64_t* __restrict__ offsets, int B,
+                                                                      int64_t max_len, int32_t* __restrict__ order) {
+  __shared__ int count[kOrderBins], start[kOrderBins];
+  const int tid = threadIdx.x;
+  auto bin = [&](int b) {  // 0: the longest
+    const int64_t len = offsets[b + 1] - offsets[b];
+    const int64_t q = len * (kOrderBins - 1) / max_len;
+    return kOrderBins - 1 - (int)(q < 0 ? 0 : q < kOrderBins ? q : kOrderBins - 1);
+  };
+  if (tid < kOrderBins) count[tid] = 0;
+  __syncthreads();
+  for (int b = tid; b < B; b += kOrderThreads) atomicAdd(&count[bin(b)], 1);
+  __syncthreads();
+  if (tid < 64) {
+    int before = 0;
+    for (int g = 0; g < kOrderBins; g += 64) {
+      int x = count[g + tid];
+      const int mine = x;
+      for (int o = 1; o < 64; o <<= 1) {
+        const int y = __shfl_up(x, o, 64);
+        if (tid >= o) x += y;
+      }
+      start[g + tid] = before + x - mine;
+      before += __shfl(x, 63, 64);
+    }
+  }
+  __syncthreads();
+  for (int b = tid; b < B; b += kOrderThreads) order[atomicAdd(&start[bin(b)], 1)] = b;
+}
+
 // One new event for one user and head: the state is read and written once,
 // 16 bytes per lane and kInFlight rows of a lane's columns at a time; LPR
 // lanes cover a row's dv columns, the block's other lanes other rows, and
@@ -786,12 +823,26 @@ void cut(int64_t groups, int64_t max_len, int dk, int* segments, int64_t* seg_le
   *segments = (int)ceil_div(max_len, *seg_len);
 }
 
+// Whether to start the longest histories first: where the device's places for
+// workgroups take a few of the gradient's roles each, the last to start decide
+// when all are done.  Measured with and without (bf16, two heads of 64,
+// ragged lengths): gradient of 256 x 400 rows 70 / 81 us, 512 x 400 136 / 145,
+// 512 x 400 of one head of 128 180 / 200, 1024 x 200 141 / 146; the forward
+// call, with more and shorter workgroups, gains nothing (1024 x 400 125 / 125)
+// and loses its neighbours' cache lines (4096 x 100 163 / 146).
+bool ordered(int64_t units, int slices, int count, int64_t B, int64_t max_len, int segments) {
+  return segments == 1 && count > 1 && B > 1 && max_len > kC && units * slices * count > 1024 &&
+         units * slices <= 2048;
+}
+
 // workspace of roles that share a contraction width and an output width
-size_t blob_bytes(int64_t units, int count, int64_t max_len, int32_t dk, int32_t dv) {
+size_t blob_bytes(int64_t B, int32_t H, int count, int64_t max_len, int32_t dk, int32_t dv) {
+  const int64_t units = B * H;
   const int vs = slice_width(dv), slices = (int)ceil_div(dv, vs);
   int segments;
   int64_t seg_len;
   cut(units * slices * count, max_len, pad_width(dk), &segments, &seg_len);
+  if (ordered(units, slices, count, B, max_len, segments)) return (size_t)round_up(4 * B, 256);
   if (segments < 2) return 0;
   return (size_t)units * segments * slices * count * pad_width(dk) * vs * 4;
 }
@@ -855,6 +906,11 @@ int launch(const Role* roles, int count, int32_t dtype, const int64_t* offsets, 
   p.inner = p.slices * count;
   cut((int64_t)p.units * p.inner, max_len, pad_width(roles[0].dk), &p.segments, &p.seg_len);
   for (int i = 0; i < count; ++i) p.roles.r[i] = roles[i];
+  if (ordered((int64_t)p.units, (int)p.slices, count, B, max_len, p.segments)) {
+    int32_t* order = static_cast<int32_t*>(ws);
+    hipLaunchKernelGGL(linattn_order_kernel, dim3(1), dim3(kOrderThreads), 0, stream, offsets, (int)B, max_len, order);
+    p.order = order;
+  }
   return dtype == DLRM_F32 ? launch_type<float>(p, stream) : launch_type<uint16_t>(p, stream);
 }
 
@@ -885,7 +941,7 @@ using namespace dlrm;
 
 extern "C" size_t dlrm_linattn_workspace_size(int64_t B, int32_t H, int64_t max_len, int32_t dk, int32_t dv) {
   if (!shape_ok(B, H, max_len, dk, dv)) return 0;
-  return blob_bytes(B * H, 1, max_len, dk, dv);
+  return blob_bytes(B, H, 1, max_len, dk, dv);
 }
 
 extern "C" int dlrm_linattn_fwd(const void* q, int64_t q_ts, int64_t q_hs, const void* k, int64_t k_ts, int64_t k_hs,
@@ -908,9 +964,9 @@ extern "C" int dlrm_linattn_fwd(const void* q, int64_t q_ts, int64_t q_hs, const
 
 extern "C" size_t dlrm_linattn_bwd_workspace_size(int64_t B, int32_t H, int64_t max_len, int32_t dk, int32_t dv) {
   if (!shape_ok(B, H, max_len, dk, dv)) return 0;
-  if (one_launch(dk, dv)) return blob_bytes(B * H, 3, max_len, dv, dk);
+  if (one_launch(dk, dv)) return blob_bytes(B, H, 3, max_len, dv, dk);
   // one after the other on the same workspace
-  const size_t two = blob_bytes(B * H, 2, max_len, dv, dk), one = blob_bytes(B * H, 1, max_len, dk, dv);
+  const size_t two = blob_bytes(B, H, 2, max_len, dv, dk), one = blob_bytes(B, H, 1, max_len, dk, dv);
   return two > one ? two : one;
 }
 

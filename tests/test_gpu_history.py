@@ -459,6 +459,28 @@ def test_linattn_long(dtype, lens, H, d):
 
 
 @pytest.mark.parametrize("dtype", [BF, FP])
+def test_linattn_bwd_many_ragged_histories(dtype):
+    """Enough short histories for the gradient to start the longest first."""
+    banner(f"linattn_bwd many histories {dtype}")
+    g = np.random.default_rng(17)
+    lens = [int(x) for x in g.integers(0, 40, 210)]
+    lens[3], lens[100], lens[209] = 131, 0, 90
+    a = Attn(18, lens, 2, 16, 16, dtype)
+    a.check_bwd(a.bwd())
+    a.check_fwd(*a.fwd())
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_linattn_max_len_may_be_loose(dtype):
+    """max_len is an upper bound: segments that no history reaches stay empty."""
+    banner(f"linattn loose max_len {dtype}")
+    a = Attn(19, [300, 5, 0, 64], 1, 64, 32, dtype)
+    a.max_len = 5000
+    a.check_fwd(*a.fwd())
+    a.check_bwd(a.bwd())
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
 def test_linattn_head_major_and_streams(dtype):
     """[heads][rows][width] storage, a stream other than the default one, and
     the same bits every time."""
