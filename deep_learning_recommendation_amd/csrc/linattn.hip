@@ -366,7 +366,9 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(Shape<
   const int64_t beg = plan.offsets[b], len = plan.offsets[b + 1] - beg;
   const int64_t s0 = seg * plan.seg_len;
   if (seg > 0 && s0 >= len) return;
-  const bool ends = plan.segments == 1 || s0 + plan.seg_len >= len;  // the history's last segment
+  // the history's last segment (the plan's last one takes what is left, also of
+  // a history longer than max_len promised)
+  const bool ends = seg == plan.segments - 1 || s0 + plan.seg_len >= len;
   if (ONLY_STATE && ends) return;
   const int64_t s1 = ends ? len : s0 + plan.seg_len;
   const int64_t blob = ((int64_t)bh * plan.segments + seg) * plan.inner + in;
@@ -641,7 +643,8 @@ __global__ __launch_bounds__(kThreads) void linattn_scan_kernel(Plan plan) {
   const int h = (int)(unit % plan.H);
   const Role& role = plan.roles.r[in / plan.slices];
   const int64_t len = plan.offsets[b + 1] - plan.offsets[b];
-  const int used = len > 0 ? (int)((len + plan.seg_len - 1) / plan.seg_len) : 1;  // segments that have rows
+  const int64_t reach = len > 0 ? (len + plan.seg_len - 1) / plan.seg_len : 1;  // segments that have rows
+  const int used = (int)(reach < plan.segments ? reach : plan.segments);
   const float l2 = log2_decay(plan.decay[h]);
   const float all = decay_pow(l2, (float)plan.seg_len);
   // the element's place in the blob (tile, thread, element) and in the state

@@ -515,7 +515,8 @@ int dlrm_add_rmsnorm_bwd(const void* dy, int64_t dy_ld, const void* dh, int64_t 
  *   q, k     dtype, row i, head h at q + i*q_ts + h*q_hs, dk contiguous
  *            elements (likewise k; v with dv elements; o with o_ts, o_hs).
  *   offsets  int64 [B + 1], non-decreasing, offsets[0] >= 0 (device).
- *   max_len  host: no history is longer (a precondition).
+ *   max_len  host: the longest history, or a bound on it.  It only cuts the
+ *            work; a loose one costs empty workgroups.
  *   decay    fp32 [H], 0 <= decay <= 1: a constant of the layer (it gets no
  *            gradient).
  *   state0   nullable fp32 [B][H][dk][dv].
@@ -525,11 +526,15 @@ int dlrm_add_rmsnorm_bwd(const void* dy, int64_t dy_ld, const void* dh, int64_t 
  *            with q, a copy of the state to bf16 (the matrix instructions'
  *            operands); the state itself is updated from exact splits of its
  *            operands and stays fp32.  DLRM_F32 multiplies in fp32.
- *   ws       dlrm_linattn_workspace_size() bytes, 256-byte aligned (may be
- *            0: then ws may be NULL).
+ *   ws       dlrm_linattn_workspace_size() bytes, 256-byte aligned (0 bytes
+ *            where no history is cut: then ws may be NULL).
+ *   A q or k that is not finite spoils what it takes part in; a v that is not
+ *            finite makes its column of o NaN from its row on, and the state's
+ *            column.  Neither reaches an earlier row or another history.
  *   Limits:  dk, dv multiples of 8, 8 .. 128; every row and head stride a
- *            multiple of 8 elements and every base 16-byte aligned; state0
- *            and state 16-byte aligned; B, H >= 1, B * H * 32 < 2^31.
+ *            multiple of 8 elements and every base 16-byte aligned; row
+ *            strides 0 .. 2^22 - 1; state0 and state 16-byte aligned;
+ *            B, H >= 1, B * H * 32 < 2^31.
  */
 size_t dlrm_linattn_workspace_size(int64_t B, int32_t H, int64_t max_len, int32_t dk, int32_t dv);
 int dlrm_linattn_fwd(const void* q, int64_t q_ts, int64_t q_hs, const void* k, int64_t k_ts, int64_t k_hs,

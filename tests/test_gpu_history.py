@@ -571,3 +571,15 @@ def test_linattn_step_pool_beyond_4_gib():
     _D().dlrm_linattn_step(x, x, x, 1, H, d, d, torch.full((H,), 0.5, device=DEV), 1.0, S,
                            torch.tensor([pool - 1], device=DEV), o)
     assert (S[pool - 1] == 1.5).all() and (o == 1.5 * d).all() and not S[0].any() and not S[pool - 2].any()
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_linattn_history_longer_than_its_bound(dtype):
+    """max_len cuts the work, it does not bound it: a longer history is whole."""
+    banner(f"linattn short max_len {dtype}")
+    a = Attn(20, [1100, 40], 1, 64, 32, dtype)
+    a.max_len = 600
+    got, back = a.fwd(), a.bwd()
+    a.max_len = 1100  # what the bounds of the sums go by
+    a.check_fwd(*got)
+    a.check_bwd(back)
