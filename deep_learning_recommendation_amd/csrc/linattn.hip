@@ -318,6 +318,7 @@ struct Plan {
   int segments;
   int64_t seg_len;  // rows per segment, a multiple of kC
   const int32_t* order;  // nullable (one segment only): the histories, longest first
+  int none;              // max_len 0: no history has a row
   Roles roles;
 };
 // The slices and roles of a unit read the same rows: they are eight blocks
@@ -363,7 +364,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(Shape<
   const int64_t bh = b * plan.H + h;
   const Role& role = plan.roles.r[in / plan.slices];
   const int col0 = (int)(in % plan.slices) * VS;
-  const int64_t beg = plan.offsets[b], len = plan.offsets[b + 1] - beg;
+  const int64_t beg = plan.offsets[b], len = plan.none ? 0 : plan.offsets[b + 1] - beg;
   const int64_t s0 = seg * plan.seg_len;
   if (seg > 0 && s0 >= len) return;
   // the history's last segment (the plan's last one takes what is left, also of
@@ -811,11 +812,12 @@ int slice_width(int32_t w) { return w <= 32 ? 32 : 64; }
 // 256 rows and with 2048 of at least 2 DK: 16 x 2500 x 4 x 64 54 -> 45 us,
 // 2 x 1500 x 2 x 64 27 -> 20 us, 1 x 1000 x 2 x 64 29 -> 19 us, gradient of
 // 4 x 5000 x 4 x 128 182 -> 140 us; at 128 rows and width 128, 1 x 20011 x 4
-// takes 72 us instead of 60.
+// takes 72 us instead of 60.  fp32 rows cost more time than their bytes, so
+// there a segment may be half as long.
 constexpr int64_t kWantGroups = 2048;
-void cut(int64_t groups, int64_t max_len, int dk, int* segments, int64_t* seg_len) {
+void cut(int64_t groups, int64_t max_len, int dk, int32_t dtype, int* segments, int64_t* seg_len) {
   int64_t want = groups > 0 ? kWantGroups / groups : 1;
-  const int64_t most = max_len / (2 * dk);
+  const int64_t most = max_len / (dtype == DLRM_F32 ? dk : 2 * dk);
   want = want < most ? want : most;
   if (want < 2) {
     *segments = 1;
@@ -838,16 +840,22 @@ bool ordered(int64_t units, int slices, int count, int64_t B, int64_t max_len, i
          units * slices <= 2048;
 }
 
-// workspace of roles that share a contraction width and an output width
-size_t blob_bytes(int64_t B, int32_t H, int count, int64_t max_len, int32_t dk, int32_t dv) {
+// workspace of roles that share a contraction width and an output width: the
+// larger of the two types' (fp32 may cut further)
+size_t scratch_bytes(int64_t B, int32_t H, int count, int64_t max_len, int32_t dk, int32_t dv) {
   const int64_t units = B * H;
   const int vs = slice_width(dv), slices = (int)ceil_div(dv, vs);
-  int segments;
-  int64_t seg_len;
-  cut(units * slices * count, max_len, pad_width(dk), &segments, &seg_len);
-  if (ordered(units, slices, count, B, max_len, segments)) return (size_t)round_up(4 * B, 256);
-  if (segments < 2) return 0;
-  return (size_t)units * segments * slices * count * pad_width(dk) * vs * 4;
+  size_t most = 0;
+  for (int32_t dtype : {DLRM_F32, DLRM_BF16}) {
+    int segments;
+    int64_t seg_len;
+    cut(units * slices * count, max_len, pad_width(dk), dtype, &segments, &seg_len);
+    size_t bytes = 0;
+    if (segments > 1) bytes = (size_t)units * segments * slices * count * pad_width(dk) * vs * 4;
+    else if (ordered(units, slices, count, B, max_len, segments)) bytes = (size_t)round_up(4 * B, 256);
+    most = bytes > most ? bytes : most;
+  }
+  return most;
 }
 
 template <class T, int DK, int VS>
@@ -905,9 +913,10 @@ int launch(const Role* roles, int count, int32_t dtype, const int64_t* offsets, 
   p.blobs = static_cast<float*>(ws);
   p.units = (unsigned)(B * H);
   p.H = (unsigned)H;
+  p.none = max_len == 0;
   p.slices = (unsigned)ceil_div(roles[0].dv, slice_width(roles[0].dv));
   p.inner = p.slices * count;
-  cut((int64_t)p.units * p.inner, max_len, pad_width(roles[0].dk), &p.segments, &p.seg_len);
+  cut((int64_t)p.units * p.inner, max_len, pad_width(roles[0].dk), dtype, &p.segments, &p.seg_len);
   for (int i = 0; i < count; ++i) p.roles.r[i] = roles[i];
   if (ordered((int64_t)p.units, (int)p.slices, count, B, max_len, p.segments)) {
     int32_t* order = static_cast<int32_t*>(ws);
@@ -944,7 +953,7 @@ using namespace dlrm;
 
 extern "C" size_t dlrm_linattn_workspace_size(int64_t B, int32_t H, int64_t max_len, int32_t dk, int32_t dv) {
   if (!shape_ok(B, H, max_len, dk, dv)) return 0;
-  return blob_bytes(B, H, 1, max_len, dk, dv);
+  return scratch_bytes(B, H, 1, max_len, dk, dv);
 }
 
 extern "C" int dlrm_linattn_fwd(const void* q, int64_t q_ts, int64_t q_hs, const void* k, int64_t k_ts, int64_t k_hs,
@@ -967,9 +976,9 @@ extern "C" int dlrm_linattn_fwd(const void* q, int64_t q_ts, int64_t q_hs, const
 
 extern "C" size_t dlrm_linattn_bwd_workspace_size(int64_t B, int32_t H, int64_t max_len, int32_t dk, int32_t dv) {
   if (!shape_ok(B, H, max_len, dk, dv)) return 0;
-  if (one_launch(dk, dv)) return blob_bytes(B, H, 3, max_len, dv, dk);
+  if (one_launch(dk, dv)) return scratch_bytes(B, H, 3, max_len, dv, dk);
   // one after the other on the same workspace
-  const size_t two = blob_bytes(B, H, 2, max_len, dv, dk), one = blob_bytes(B, H, 1, max_len, dk, dv);
+  const size_t two = scratch_bytes(B, H, 2, max_len, dv, dk), one = scratch_bytes(B, H, 1, max_len, dk, dv);
   return two > one ? two : one;
 }
 

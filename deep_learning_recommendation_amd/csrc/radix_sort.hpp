@@ -208,6 +208,59 @@ __global__ __launch_bounds__(RT) void tile_offset_kernel(const uint32_t* __restr
   }
 }
 
+// The same offsets where there are few tiles, without the chunk sums: the
+// block of digit group blockIdx.y adds up all tiles' counts of the digits
+// below its own.  One launch less per pass, which is what few keys cost; but
+// the last group reads every count.  A table gradient of 72175 tokens (18
+// tiles, two passes of 10 bits) takes 61 us with it and 67 without, one of
+// 250000 (62 tiles) 70 and 60.
+constexpr int kFewThreads = 1024, kFewTiles = 32;
+static_assert(kFewTiles <= kChunk, "a chunk holds the few tiles");
+template <int DB>
+__global__ __launch_bounds__(kFewThreads) void tile_offset_few_kernel(const uint32_t* __restrict__ counts, int tiles,
+                                                                      uint32_t* __restrict__ offsets, Clear clear) {
+  if (clear.mine()) return clear.run();
+  constexpr int NB = 1 << DB, W = kFewThreads / 64, PER = kFewTiles / W;  // tiles per wave
+  __shared__ uint32_t part[W][64], below_part[W];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int below = blockIdx.y * 64;
+  const int dg = below + lane;
+  uint32_t v[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) v[i] = wave * PER + i < tiles ? counts[(int64_t)(wave * PER + i) * NB + dg] : 0u;
+  uint32_t sum = 0;
+  for (int t = wave; t < tiles; t += W)
+#pragma unroll 8
+    for (int d = lane; d < below; d += 64) sum += counts[(int64_t)t * NB + d];
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) sum += __shfl_xor(sum, o, 64);
+  if (lane == 0) below_part[wave] = sum;
+  uint32_t mine = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) mine += v[i];
+  part[wave][lane] = mine;
+  __syncthreads();
+  uint32_t base = 0, total = 0, earlier = 0;
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    base += below_part[w];
+    total += part[w][lane];
+    if (w < wave) earlier += part[w][lane];
+  }
+  uint32_t incl = total;  // digits of the group, lane by lane
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const uint32_t y = __shfl_up(incl, o, 64);
+    if (lane >= o) incl += y;
+  }
+  base += incl - total + earlier;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    if (wave * PER + i < tiles) offsets[(int64_t)(wave * PER + i) * NB + dg] = base;
+    base += v[i];
+  }
+}
+
 // One pass: stable scatter of tile blockIdx.x by the digit at `shift`.  The
 // rank of a key is (its digit's count in earlier waves) + (in earlier items
 // of its wave) + (in lower lanes of its item), the last from DB ballots.
@@ -321,24 +374,31 @@ SortPlan sort_plan(int key_bits, int max_digit_bits) {
 // Every pass of the plan over keys[0] / vals[0]; the sorted pairs end in
 // buffer passes % 2, which is returned.  counts and offsets hold tiles
 // rows of 1 << digit_bits words, sums one such row per kChunk tiles.  `clear`
-// is what is left to clear, over 4 launches a pass.
+// is what is left to clear, shared out over the launches.
 int launch_sort(const SortPlan& plan, uint32_t* const (&keys)[2], int32_t* const (&vals)[2], uint32_t* counts,
                 uint32_t* sums, uint32_t* offsets, int n, hipStream_t stream, ClearParts clear = ClearParts()) {
   const unsigned tiles = (unsigned)ceil_div(n, TILE);
   const dim3 tile_grid(tiles);
   const dim3 chunk_grid((unsigned)ceil_div(tiles, kChunk), (unsigned)((1 << plan.digit_bits) / 64));
-  clear.launches = 4 * plan.passes;
+  const bool few = tiles <= kFewTiles;
+  clear.launches = (few ? 3 : 4) * plan.passes;
   int cur = 0;
   for (int pass = 0; pass < plan.passes; ++pass) {
     const int shift = pass * plan.digit_bits;
     dim3 grid[4] = {tile_grid, chunk_grid, chunk_grid, tile_grid};
     Clear c[4];
-    for (int i = 0; i < 4; ++i) c[i] = clear.next(&grid[i]);
+    for (int i = 0; i < 4; ++i)
+      if (i != 1 || !few) c[i] = clear.next(&grid[i]);
 #define DLRM_PASS(DB)                                                                                               \
   hipLaunchKernelGGL(tile_hist_kernel<DB>, grid[0], dim3(RT), 0, stream, keys[cur], n, shift, counts, c[0]);       \
-  hipLaunchKernelGGL(chunk_sum_kernel<DB>, grid[1], dim3(RT), 0, stream, counts, (int)tiles, sums, c[1]);          \
-  hipLaunchKernelGGL(tile_offset_kernel<DB>, grid[2], dim3(RT), 0, stream, counts, sums, (int)tiles, offsets,      \
-                     c[2]);                                                                                        \
+  if (few) {                                                                                                       \
+    hipLaunchKernelGGL(tile_offset_few_kernel<DB>, grid[2], dim3(kFewThreads), 0, stream, counts, (int)tiles,      \
+                       offsets, c[2]);                                                                             \
+  } else {                                                                                                         \
+    hipLaunchKernelGGL(chunk_sum_kernel<DB>, grid[1], dim3(RT), 0, stream, counts, (int)tiles, sums, c[1]);        \
+    hipLaunchKernelGGL(tile_offset_kernel<DB>, grid[2], dim3(RT), 0, stream, counts, sums, (int)tiles, offsets,    \
+                       c[2]);                                                                                      \
+  }                                                                                                                \
   hipLaunchKernelGGL(scatter_kernel<DB>, grid[3], dim3(RT), 0, stream, keys[cur], vals[cur], keys[cur ^ 1],        \
                      vals[cur ^ 1], n, shift, offsets, c[3])
     if (plan.digit_bits == 10) {

@@ -112,7 +112,7 @@ __global__ __launch_bounds__(256) void token_keys_kernel(const int64_t* __restri
 // scatter_kernel, digit by digit) while the others clear the table gradient.
 // One launch instead of the nine of two global passes, whose time would all
 // be launches.
-constexpr int kSmallThreads = 1024, kSmallItems = 8, kSmallMax = kSmallThreads * kSmallItems;
+constexpr int kSmallThreads = 1024, kSmallItems = 16, kSmallMax = kSmallThreads * kSmallItems;
 __global__ __launch_bounds__(kSmallThreads) void token_sort_small_kernel(const int64_t* __restrict__ tokens, int n,
                                                                          int64_t rows, int key_bits,
                                                                          uint32_t* __restrict__ keys,

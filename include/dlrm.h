@@ -516,7 +516,8 @@ int dlrm_add_rmsnorm_bwd(const void* dy, int64_t dy_ld, const void* dh, int64_t 
  *            elements (likewise k; v with dv elements; o with o_ts, o_hs).
  *   offsets  int64 [B + 1], non-decreasing, offsets[0] >= 0 (device).
  *   max_len  host: the longest history, or a bound on it.  It only cuts the
- *            work; a loose one costs empty workgroups.
+ *            work; a loose one costs empty workgroups.  0: no history has a
+ *            row (q, k, v and o may be NULL).
  *   decay    fp32 [H], 0 <= decay <= 1: a constant of the layer (it gets no
  *            gradient).
  *   state0   nullable fp32 [B][H][dk][dv].
