@@ -398,7 +398,6 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(Shape<
   const uint32_t koff = (uint32_t)((back ? kC - KR * (KN - 1) - 1 - kr : kr) * (int)role.k.ts + kc) * sizeof(T);
   const uint32_t voff = (uint32_t)((back ? kC - VR * (VN - 1) - 1 - vr : vr) * (int)role.v.ts + col0 + vc) * sizeof(T);
   const uint32_t qoff = (uint32_t)(place(16 * wave + n) * (int)role.q.ts + g * (M::kWide / 4)) * sizeof(T);
-  const uint32_t ooff = (uint32_t)(place(16 * wave + n) * (int)role.o.ts + col0 + (VS / 4) * g) * sizeof(T);
   const bool full_width = dk == DK && col0 + VS <= dv;
   uint4 kreg[KN], vreg[VN];
   auto fetch = [&](int64_t c0) {
@@ -525,7 +524,9 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(Shape<
     // made from copies in each chunk: kept outside the loop, the weights would
     // cost registers
     const float tile_decay = local_copy(d16), lag = local_copy((float)(n - 4 * g));
-    if (!ONLY_STATE) {
+    const int empty = kC - m;  // tiles of empty places only are passed over
+    const bool has_rows = 16 * wave + 16 > empty;
+    if (!ONLY_STATE && has_rows) {
       // the masked, decayed products of this wave's 16 rows with the chunk's
       f32x4 p[4];
       f32x4 w;  // of the tile before the diagonal, then of the ones before that
@@ -535,7 +536,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(Shape<
 #pragma unroll
       for (int i = 3; i >= 0; --i) {
         p[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (i > wave) continue;  // above the diagonal
+        if (i > wave || 16 * i + 16 <= empty) continue;  // above the diagonal, or empty
 #pragma unroll
         for (int f = 0; f < QN; ++f) p[i] = M::mma(M::wide(Ks + (16 * i + n) * PK + f * M::kWide, g), qf[f], p[i]);
         if (i == wave) {
@@ -557,7 +558,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(Shape<
 #pragma unroll
         for (int j = 0; j < NT; ++j) out[j] = M::mma(M::wide(Ss + (16 * j + n) * PK + f * M::kWide, g), qf[f], out[j]);
       // (an empty place's power may be any; its row is not stored)
-      const float from_state = oscale * decay_pow(l2, local_copy((float)n) + (float)(16 * wave - (kC - m) + lead));
+      const float from_state = oscale * decay_pow(l2, local_copy((float)n) + (float)(16 * wave - empty + lead));
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -565,16 +566,18 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(Shape<
       if (c0 + kC < s1) fetch_q(c0 + kC);
     }
     const float nan = __builtin_nanf("");
-    if (!ONLY_STATE) {
+    if (!ONLY_STATE && has_rows) {
 #pragma unroll
       for (int f = 0; f < 4 / M::kTiles; ++f) {
-        if (f * M::kTiles > wave) continue;  // above the diagonal
+        if (f * M::kTiles > wave || 16 * M::kTiles * (f + 1) <= empty) continue;
 #pragma unroll
         for (int j = 0; j < NT; ++j)
           out[j] = M::mma(M::template time<PV>(Vs, f, lane, M::time_col(lane, VS / 4) + 4 * j), pf[f], out[j]);
       }
-      if (16 * wave + n >= kC - m) {
-        char* row = const_cast<char*>(window(role.o, c0 - (kC - m))) + local_copy(ooff);
+      if (16 * wave + n >= empty) {
+        const int ln = local_copy(lane);
+        char* row = const_cast<char*>(window(role.o, c0 - empty)) +
+                    (uint32_t)(place(16 * wave + (ln & 15)) * (int)role.o.ts + col0 + (VS / 4) * (ln >> 4)) * sizeof(T);
         if (any_bad) {
           const int cold = local_copy(lane);
 #pragma unroll
@@ -598,6 +601,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(Shape<
         for (int r = 0; r < 4; ++r) S.t[i][j][r] *= all;
 #pragma unroll
     for (int f = 0; f < 4 / M::kTiles; ++f) {
+      if (16 * M::kTiles * (f + 1) <= empty) continue;
       Frag vf[Sh::kNW];
 #pragma unroll
       for (int j = 0; j < Sh::kNW; ++j)
