@@ -6,7 +6,10 @@
 //
 // Lookup.  Bound by memory: n rows read (a popular row from cache), n rows
 // written, eight bytes of token each.  A group of lanes covers one row with
-// 16-byte pieces, and each group keeps kRows rows in flight.
+// 16-byte pieces, and each group keeps kRows rows in flight (2 and 8 measured
+// up to 4% slower).  819200 tokens x 128 bf16, Zipf(1.2) over 1M rows: 36 us,
+// 210 MB written at 5.8 TB/s; 409600 x 128 fp32, uniform: 61 us, 7.0 TB/s of
+// reads and writes.
 //
 // Gradient.  The positions are sorted by token (radix_sort.hpp: stable, so a
 // row's positions stay in order), which turns the scattered sums into runs.
@@ -17,7 +20,11 @@
 // is added up in LDS within its block; one that crosses blocks leaves a
 // partial sum per block (head: it began earlier; tail: it begins here and
 // goes on), and a second kernel adds a run's partials in a fixed order.
-// Every row is written once, by one group: no atomics.
+// Every row is written once, by one group: no atomics.  The sort's launches
+// wait on each other and leave memory idle, so they clear the table gradient
+// on the side.  819200 tokens x 128 bf16 into 1M fp32 rows: 176 us, 728 MB at
+// 4.1 TB/s (sort and clear 108, sums 55, join 9); 2561 tokens x 16: 18.6 us,
+// three dependent launches.
 #include "common.hpp"
 #include "radix_sort.hpp"
 #include "rows.hpp"
@@ -110,8 +117,8 @@ __global__ __launch_bounds__(256) void token_keys_kernel(const int64_t* __restri
 
 // Few tokens: one block does the whole sort in LDS (the ranking of
 // scatter_kernel, digit by digit) while the others clear the table gradient.
-// One launch instead of the nine of two global passes, whose time would all
-// be launches.
+// One launch instead of the seven of two global passes, whose time would all
+// be launches (2561 tokens: 11 us; 9724 tokens, whole gradient, 45 -> 32 us).
 constexpr int kSmallThreads = 1024, kSmallItems = 16, kSmallMax = kSmallThreads * kSmallItems;
 __global__ __launch_bounds__(kSmallThreads) void token_sort_small_kernel(const int64_t* __restrict__ tokens, int n,
                                                                          int64_t rows, int key_bits,
