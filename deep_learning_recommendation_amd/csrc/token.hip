@@ -23,7 +23,7 @@
 // Every row is written once, by one group: no atomics.  The sort's launches
 // wait on each other and leave memory idle, so they clear the table gradient
 // on the side.  819200 tokens x 128 bf16 into 1M fp32 rows: 176 us, 728 MB at
-// 4.1 TB/s (sort and clear 108, sums 55, join 9); 2561 tokens x 16: 18.6 us,
+// 4.1 TB/s (sort and clear 108, sums 55, join 9); 2561 tokens x 16: 16.5 us,
 // three dependent launches.
 #include "common.hpp"
 #include "radix_sort.hpp"
@@ -118,17 +118,22 @@ __global__ __launch_bounds__(256) void token_keys_kernel(const int64_t* __restri
 // Few tokens: one block does the whole sort in LDS (the ranking of
 // scatter_kernel, digit by digit) while the others clear the table gradient.
 // One launch instead of the seven of two global passes, whose time would all
-// be launches (2561 tokens: 11 us; 9724 tokens, whole gradient, 45 -> 32 us).
-constexpr int kSmallThreads = 1024, kSmallItems = 16, kSmallMax = kSmallThreads * kSmallItems;
+// be launches.  Key bits are dealt evenly to the digits, since a digit's bits
+// are what its ranking costs (whole gradient, 15000 tokens of 19 bits: 61 us
+// with digits of 8, 8 and 3 bits, 56 with 7, 7 and 5); up to 4096 tokens take
+// the kernel with 4 positions a thread, which holds fewer registers and less
+// LDS than that with 16 (2561 tokens: 18.5 -> 16.4 us).
+constexpr int kSmallThreads = 1024, kSmallMax = kSmallThreads * 16;
+template <int ITEMS>
 __global__ __launch_bounds__(kSmallThreads) void token_sort_small_kernel(const int64_t* __restrict__ tokens, int n,
                                                                          int64_t rows, int key_bits,
                                                                          uint32_t* __restrict__ keys,
                                                                          int32_t* __restrict__ vals, Clear clear) {
   constexpr int NB = 256, W = kSmallThreads / 64;
-  __shared__ uint32_t lk[kSmallMax];
-  __shared__ int32_t lv[kSmallMax];
+  __shared__ uint32_t lk[kSmallThreads * ITEMS];
+  __shared__ int32_t lv[kSmallThreads * ITEMS];
   __shared__ uint32_t cnt[W][NB];
-  __shared__ uint32_t tot[NB / 64];
+  __shared__ uint32_t start[NB], tot[NB / 64];
   if (clear.mine()) return clear.run();
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const uint64_t below = (lane == 0) ? 0ull : (~0ull >> (64 - lane));
@@ -139,21 +144,22 @@ __global__ __launch_bounds__(kSmallThreads) void token_sort_small_kernel(const i
       lk[pos(i)] = token_key(tokens[pos(i)], rows);
       lv[pos(i)] = pos(i);
     }
-  for (int shift = 0; shift < key_bits; shift += 8) {
+  const int passes = (key_bits + 7) / 8, digit = (key_bits + passes - 1) / passes;
+  const uint32_t mask = (1u << digit) - 1u;
+  for (int shift = 0; shift < key_bits; shift += digit) {
     for (int i = tid; i < W * NB; i += kSmallThreads) (&cnt[0][0])[i] = 0u;
     __syncthreads();
-    uint32_t key[kSmallItems], rank[kSmallItems];
-    int32_t val[kSmallItems];
+    uint32_t key[ITEMS], rank[ITEMS];
+    int32_t val[ITEMS];
 #pragma unroll
-    for (int i = 0; i < kSmallItems; ++i) {
+    for (int i = 0; i < ITEMS; ++i) {
       if (i >= items) break;
       const bool valid = pos(i) < n;
       key[i] = valid ? lk[pos(i)] : 0u;
       val[i] = valid ? lv[pos(i)] : 0;
-      const uint32_t dg = (key[i] >> shift) & (NB - 1);
+      const uint32_t dg = (key[i] >> shift) & mask;
       uint64_t peers = __ballot(valid);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
+      for (int q = 0; q < digit; ++q) {
         const bool bit = (dg >> q) & 1u;
         const uint64_t m = __ballot(bit);
         peers &= bit ? m : ~m;
@@ -163,14 +169,16 @@ __global__ __launch_bounds__(kSmallThreads) void token_sort_small_kernel(const i
       if (valid && (peers & below) == 0ull) cnt[wave][dg] = before + (uint32_t)__popcll(peers);
     }
     __syncthreads();
-    // a digit's start, then each wave's within it
+    // each wave's start within a digit, and the digits' own starts
     uint32_t run = 0, incl = 0;
     if (tid < NB) {
+      uint32_t c[W];
+#pragma unroll
+      for (int w = 0; w < W; ++w) c[w] = cnt[w][tid];
 #pragma unroll
       for (int w = 0; w < W; ++w) {
-        const uint32_t c = cnt[w][tid];
         cnt[w][tid] = run;
-        run += c;
+        run += c[w];
       }
       incl = run;
 #pragma unroll
@@ -179,20 +187,17 @@ __global__ __launch_bounds__(kSmallThreads) void token_sort_small_kernel(const i
         if (lane >= o) incl += y;
       }
       if (lane == 63) tot[wave] = incl;
-    }
-    __syncthreads();
-    if (tid < NB) {
-      uint32_t start = incl - run;
-      for (int w = 0; w < wave; ++w) start += tot[w];
-#pragma unroll
-      for (int w = 0; w < W; ++w) cnt[w][tid] += start;
+      start[tid] = incl - run;  // within the digit's group of 64
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kSmallItems; ++i) {
+    for (int i = 0; i < ITEMS; ++i) {
       if (i >= items) break;
       if (pos(i) < n) {
-        const uint32_t to = cnt[wave][(key[i] >> shift) & (NB - 1)] + rank[i];
+        const uint32_t dg = (key[i] >> shift) & mask;
+        uint32_t to = cnt[wave][dg] + start[dg] + rank[i];
+#pragma unroll
+        for (int g = 0; g < NB / 64 - 1; ++g) to += g < (int)(dg >> 6) ? tot[g] : 0u;
         lk[to] = key[i];
         lv[to] = val[i];
       }
@@ -540,8 +545,12 @@ extern "C" int dlrm_token_embed_bwd(const int64_t* tokens, int64_t n, const void
   if (n <= kSmallMax) {
     dim3 grid(1);
     const Clear c = clear.next(&grid);
-    hipLaunchKernelGGL(token_sort_small_kernel, grid, dim3(kSmallThreads), 0, stream, tokens, (int)n, rows,
-                       bits_for(rows), keys[0], vals[0], c);
+    if (n <= 4 * kSmallThreads)
+      hipLaunchKernelGGL(token_sort_small_kernel<4>, grid, dim3(kSmallThreads), 0, stream, tokens, (int)n, rows,
+                         bits_for(rows), keys[0], vals[0], c);
+    else
+      hipLaunchKernelGGL(token_sort_small_kernel<16>, grid, dim3(kSmallThreads), 0, stream, tokens, (int)n, rows,
+                         bits_for(rows), keys[0], vals[0], c);
     if (n == 0) return launch_status();
   } else {
     const int64_t blocks = ceil_div(n, 256);

@@ -130,6 +130,19 @@ def test_token_embed_bwd_exact_on_integers_and_repeatable():
     assert torch.equal(a.cpu().double(), R.embed_grad(tok, dout.cpu(), rows, 2.0)[0])
 
 
+@pytest.mark.parametrize("n", [63, 1024, 1025, 4096, 4097, 16384, 16385])
+@pytest.mark.parametrize("rows", [1, 255, 256, 70001, 1 << 20])
+def test_token_embed_bwd_sizes_of_the_sort(n, rows):
+    """Every count of key bits and positions a thread at which the sort
+    changes; sums of integers are exact."""
+    banner(f"token_embed_bwd sort {n} {rows}")
+    g = torch.Generator().manual_seed(n + rows)
+    tok = torch.randint(0, rows + 2, (n,), generator=g) - 1  # the ends are out of range
+    dout = torch.randint(-8, 9, (n, 8), generator=g).float().to(DEV)
+    dT = _bwd(tok, dout, rows, 8, 2.0, torch.full((rows, 8), float("nan"), device=DEV), False)
+    assert torch.equal(dT.cpu().double(), R.embed_grad(tok, dout.cpu(), rows, 2.0)[0])
+
+
 def test_token_embed_empty():
     banner("token_embed empty")
     D = _D()
