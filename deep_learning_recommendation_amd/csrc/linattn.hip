@@ -331,7 +331,7 @@ struct Plan {
 // The slices and roles of a unit read the same rows: they are eight blocks
 // apart, on one XCD and next to each other in time.
 __device__ __forceinline__ bool locate(const Plan& p, unsigned units, unsigned* unit, unsigned* in) {
-  const unsigned k = blockIdx.x >> 3;
+  const unsigned k = (unsigned)block_number() >> 3;  // (kGridX is a multiple of 8)
   *unit = k / p.inner * 8 + (blockIdx.x & 7);
   *in = k % p.inner;
   return *unit < units;
@@ -725,14 +725,17 @@ __global__ __launch_bounds__(kOrderThreads) void linattn_order_kernel(const int6
 // TB/s (one thread per column: 768 us).
 constexpr int kInFlight = 4;
 template <class T, int LPR>
-__global__ __launch_bounds__(kThreads) void linattn_step_kernel(Strided q, Strided k, Strided v, Strided o, int H, int dk,
-                                                                int dv, const float* __restrict__ decay, float scale,
+__global__ __launch_bounds__(kThreads) void linattn_step_kernel(Strided q, Strided k, Strided v, Strided o,
+                                                                int64_t pairs, int H, int dk, int dv,
+                                                                const float* __restrict__ decay, float scale,
                                                                 float* __restrict__ state,
                                                                 const int64_t* __restrict__ slots) {
   constexpr int RPB = kThreads / LPR;  // rows side by side
   __shared__ f32x4 part[kThreads / 64][LPR];
-  const int64_t b = blockIdx.x / (unsigned)H;
-  const int h = (int)(blockIdx.x % (unsigned)H);
+  const unsigned pair = (unsigned)block_number();
+  if (pair >= pairs) return;
+  const int64_t b = pair / (unsigned)H;
+  const int h = (int)(pair % (unsigned)H);
   const int64_t slot = slots ? slots[b] : b;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c = (threadIdx.x & (LPR - 1)) * 4, r0 = threadIdx.x / LPR;
@@ -891,11 +894,11 @@ int launch_shape(const Plan& plan, hipStream_t stream) {
       done[dev] = true;
     }
   }
-  auto blocks = [&](int64_t units) { return dim3((unsigned)(ceil_div(units, 8) * 8 * plan.inner)); };
+  auto blocks = [&](int64_t units) { return grid_of(ceil_div(units, 8) * 8 * plan.inner); };
   if (plan.segments > 1) {
     hipLaunchKernelGGL((linattn_kernel<T, DK, VS, true>), blocks(plan.units * (plan.segments - 1)), dim3(kThreads), lds,
                        stream, plan);
-    dim3 scan = blocks(plan.units);
+    dim3 scan = blocks(plan.units);  // (cut histories are fewer than kWantGroups)
     scan.y = Shape<T, DK, VS>::kBlob;
     hipLaunchKernelGGL((linattn_scan_kernel<T, DK, VS>), scan, dim3(kThreads), 0, stream, plan);
   }
@@ -942,10 +945,10 @@ int launch(const Role* roles, int count, int32_t dtype, const int64_t* offsets, 
 template <class T>
 int launch_step(const Strided& q, const Strided& k, const Strided& v, const Strided& o, int64_t B, int32_t H, int32_t dk,
                 int32_t dv, const float* decay, float scale, float* state, const int64_t* slots, hipStream_t stream) {
-  const dim3 grid((unsigned)(B * H)), block(kThreads);
+  const dim3 grid = grid_of(B * H), block(kThreads);
 #define DLRM_STEP(L)                                                                                                  \
-  hipLaunchKernelGGL((linattn_step_kernel<T, L>), grid, block, 0, stream, q, k, v, o, H, dk, dv, decay, scale, state, \
-                     slots)
+  hipLaunchKernelGGL((linattn_step_kernel<T, L>), grid, block, 0, stream, q, k, v, o, B * H, H, dk, dv, decay, scale, \
+                     state, slots)
   if (dv <= 16) DLRM_STEP(4);
   else if (dv <= 32) DLRM_STEP(8);
   else if (dv <= 64) DLRM_STEP(16);

@@ -13,6 +13,15 @@ inline bool rows_aligned(const void* p, int64_t ld, size_t elem, size_t bytes) {
   return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0 && (((size_t)ld * elem) & (bytes - 1)) == 0;
 }
 
+// Blocks of a launch that may have more of them than one dimension takes (its
+// work-items have to stay below 2^32): numbered along x, then along z.
+constexpr unsigned kGridX = 1u << 20;
+inline dim3 grid_of(int64_t blocks) {
+  return blocks <= kGridX ? dim3((unsigned)blocks) : dim3(kGridX, 1, (unsigned)ceil_div(blocks, kGridX));
+}
+constexpr int64_t kMaxGrid = (int64_t)kGridX * 65535;
+__device__ __forceinline__ int64_t block_number() { return (int64_t)blockIdx.z * gridDim.x + blockIdx.x; }
+
 // Stores that pass the caches: an output is written once and is as large as
 // what the caches hold, or larger; kept there, it would only delay the inputs
 // behind it.  Measured: dropout of 819200 x 128 bf16 74 -> 58 us, residual +

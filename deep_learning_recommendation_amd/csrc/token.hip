@@ -49,7 +49,7 @@ __global__ __launch_bounds__(256) void token_fwd_kernel(const TI* __restrict__ t
                                                         TO* __restrict__ out, int64_t out_ld, int g_log2) {
   const int GL = 1 << g_log2, gl = threadIdx.x & (GL - 1);
   const int64_t groups = 256 >> g_log2;
-  const int64_t i0 = ((int64_t)blockIdx.x * groups + (threadIdx.x >> g_log2)) * kRows;
+  const int64_t i0 = (block_number() * groups + (threadIdx.x >> g_log2)) * kRows;
   if (i0 >= n) return;
   // a token that names no row reads row 0 and writes zeros: no branch splits
   // the batch of loads
@@ -84,8 +84,8 @@ int launch_fwd(const void* table, int64_t rows, int d, const int64_t* tokens, in
                int64_t out_ld, hipStream_t stream) {
   const int g = group_log2(d / VE);
   const int64_t blocks = ceil_div(n, (int64_t)(256 >> g) * kRows);
-  if (blocks > 0x7fffffffLL) return DLRM_E_UNSUPPORTED;
-  hipLaunchKernelGGL((token_fwd_kernel<TI, TO, VE>), dim3((unsigned)blocks), dim3(256), 0, stream,
+  if (blocks > kMaxGrid) return DLRM_E_UNSUPPORTED;
+  hipLaunchKernelGGL((token_fwd_kernel<TI, TO, VE>), grid_of(blocks), dim3(256), 0, stream,
                      static_cast<const TI*>(table), rows, d, tokens, n, scale, static_cast<TO*>(out), out_ld, g);
   return launch_status();
 }

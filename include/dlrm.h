@@ -573,7 +573,7 @@ int dlrm_linattn_bwd(const void* q, int64_t q_ts, int64_t q_hs, const void* k, i
  *   slots    nullable int64 [B], distinct: user b's entry of the pool (NULL:
  *            b).  A negative slot marks no user: o is +0, no state changes.
  *   Limits:  dk, dv multiples of 8, 8 .. 128; bases and strides as above;
- *            the pool may hold more than 2^32 bytes.
+ *            B * H * 32 < 2^31; the pool may hold more than 2^32 bytes.
  */
 int dlrm_linattn_step(const void* q, int64_t q_bs, int64_t q_hs, const void* k, int64_t k_bs, int64_t k_hs,
                       const void* v, int64_t v_bs, int64_t v_hs, int32_t dtype, int64_t B, int32_t H, int32_t dk,

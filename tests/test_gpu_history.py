@@ -596,3 +596,81 @@ def test_linattn_history_longer_than_its_bound(dtype):
     a.max_len = 1100  # what the bounds of the sums go by
     a.check_fwd(*got)
     a.check_bwd(back)
+
+
+# Launches of more blocks than one grid dimension takes (2^20 of them).
+
+def test_token_embed_fwd_many_rows():
+    banner("token_embed_fwd 2^26 rows")
+    n, rows, d = (1 << 26) + 5, 1000, 68
+    T = torch.randn(rows, d, generator=torch.Generator().manual_seed(3)).to(BF).to(DEV)
+    tok = torch.randint(0, rows, (n,), device=DEV)
+    out = torch.empty((n, d), dtype=BF, device=DEV)
+    _D().dlrm_token_embed_fwd(T, rows, d, tok, n, 1.0, out, d)
+    for i in range(0, n, 1 << 23):
+        assert torch.equal(out[i:i + (1 << 23)], T[tok[i:i + (1 << 23)]])
+
+
+def _two_steps(q, k, v, do, off, S0, dS, lam):
+    """Histories of at most two rows, all at once: o, the states, dq, dk, dv and dS0."""
+    len_ = off[1:] - off[:-1]
+    S, states, o = S0, [], torch.zeros_like(v)
+    dq, dk, dv = torch.zeros_like(q), torch.zeros_like(k), torch.zeros_like(v)
+    rows = [(len_ > t, off[:-1] + t) for t in range(2)]
+    for on, at in rows:
+        i = at[on]
+        S = S.clone()
+        S[on] = lam * S[on] + k[i, :, None] * v[i, None, :]
+        o[i] = (q[i, :, None] * S[on]).sum(1)
+        dq[i] = (S[on] * do[i, None, :]).sum(2)
+        states.append(S)
+    W = dS
+    for on, at in rows[::-1]:
+        i = at[on]
+        U = W[on] + q[i, :, None] * do[i, None, :]
+        dk[i] = (U * v[i, None, :]).sum(2)
+        dv[i] = (U * k[i, :, None]).sum(1)
+        W = W.clone()
+        W[on] = lam * U
+    return o, S, dq, dk, dv, W
+
+
+def test_linattn_many_histories():
+    """Sums of at most 2 * 8 + 2 terms, whose weights (a power of the decay and
+    its products) are within 8 u32: every output is within 32 u32 of its
+    terms' magnitudes."""
+    banner("linattn 2^20 histories")
+    D, B, w = _D(), (1 << 20) + 5, 8
+    g = torch.Generator().manual_seed(4)
+    off = torch.zeros(B + 1, dtype=torch.int64)
+    off[1:] = torch.randint(0, 3, (B,), generator=g).cumsum(0)
+    n = int(off[-1])
+    q, k, v, do = (torch.randn(n, 1, w, generator=g).to(DEV) for _ in range(4))
+    S0, dS = (torch.randn(B, 1, w, w, generator=g).to(DEV) for _ in range(2))
+    off, lam = off.to(DEV), torch.tensor([0.75], device=DEV)
+    o, dq, dk, dv = (torch.empty_like(x) for x in (q, q, k, v))
+    S, dS0 = torch.empty_like(S0), torch.empty_like(S0)
+    D.dlrm_linattn_fwd(q, k, v, off, B, 1, 2, w, w, lam, 1.0, S0, o, S, _ws(D.dlrm_linattn_workspace_size(B, 1, 2, w, w)))
+    D.dlrm_linattn_bwd(q, k, v, do, off, B, 1, 2, w, w, lam, 1.0, S0, dS, dq, dk, dv, dS0,
+                       _ws(D.dlrm_linattn_bwd_workspace_size(B, 1, 2, w, w)))
+    args = [x.double().squeeze(1) for x in (q, k, v, do)], [x.double().squeeze(1) for x in (S0, dS)]
+    want = _two_steps(*args[0], off, *args[1], 0.75)
+    mag = _two_steps(*[x.abs() for x in args[0]], off, *[x.abs() for x in args[1]], 0.75)
+    for name, got, ref, m in zip("o S dq dk dv dS0".split(), (o, S, dq, dk, dv, dS0), want, mag):
+        err = (got.squeeze(1).double() - ref).abs()
+        assert bool((err <= 32 * U32 * m).all()), (name, float((err / m.clamp_min(1e-30)).max()))
+
+
+@pytest.mark.parametrize("dtype", [FP, BF])
+def test_linattn_step_many_users(dtype):
+    """Small integers and a decay of 1/2: every sum is exact."""
+    banner(f"linattn_step 2^20 users and heads {dtype}")
+    B, H, w = (1 << 19) + 3, 2, 8
+    g = torch.Generator().manual_seed(6)
+    q, k, v = (torch.randint(-1, 2, (B, H, w), generator=g).to(dtype).to(DEV) for _ in range(3))
+    S = torch.randint(-2, 3, (B, H, w, w), generator=g).float().to(DEV)
+    want = 0.5 * S + k.float()[..., None] * v.float()[:, :, None, :]
+    o = torch.empty((B, H, w), dtype=dtype, device=DEV)
+    _D().dlrm_linattn_step(q, k, v, B, H, w, w, torch.full((H,), 0.5, device=DEV), 1.0, S, None, o)
+    assert torch.equal(S, want)
+    assert torch.equal(o, (q.float()[..., None] * want).sum(2).to(dtype))
