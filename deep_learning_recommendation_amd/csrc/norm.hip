@@ -77,6 +77,24 @@ struct Out<int8_t, VE> {
   }
 };
 
+// An int8 row's scale from its largest magnitude (as bits), and the factor
+// that turns its elements into steps.  Scales below 2^-120 have a reciprocal
+// that may overflow, or too few bits for 127 steps to reach the largest
+// element: there the elements are taken 2^100 times, up to `limit`.
+constexpr float kTinyUnit = 0x1p-120f, kTinyUp = 0x1p100f;
+struct RowScale {
+  float unit, inv, limit;
+  __device__ __forceinline__ explicit RowScale(uint32_t top) {
+    unit = __uint_as_float(top) / 127.f;
+    const float up = tiny() ? kTinyUp : 1.f;
+    inv = unit > 0.f ? 1.f / (unit * up) : 0.f;
+    limit = 127.f * (unit * up);
+  }
+  __device__ __forceinline__ bool tiny() const { return unit < kTinyUnit; }
+  __device__ __forceinline__ float scaled(float v) const { return fminf(fmaxf(v * kTinyUp, -limit), limit); }
+  __device__ __forceinline__ float steps(float v) const { return unit > 0.f ? rintf(v * inv) : 0.f; }
+};
+
 // bit j: element e + j is kept (VE of them, e a multiple of VE, VE divides 8)
 template <int VE>
 __device__ __forceinline__ uint32_t keep_piece(const DropState& st, int64_t e, uint32_t cut) {
@@ -172,13 +190,18 @@ __global__ __launch_bounds__(kThreads) void addnorm_fwd_kernel(Fwd a) {
           for (int j = 0; j < VE; ++j) top = Top()(top, __float_as_uint(v[i][j]) & 0x7fffffffu);
         }
       top = G::reduce(top, Top());
-      const float unit = __uint_as_float(top) / 127.f;
-      const float inv = unit > 0.f ? 1.f / unit : 0.f;
-      if (G::lane() == 0) *reinterpret_cast<float2*>(a.scale_bias + 2 * row) = make_float2(unit, 0.f);
+      const RowScale s(top);
+      if (G::lane() == 0) *reinterpret_cast<float2*>(a.scale_bias + 2 * row) = make_float2(s.unit, 0.f);
+      if (s.tiny()) {
+#pragma unroll
+        for (int i = 0; i < NP; ++i)
+#pragma unroll
+          for (int j = 0; j < VE; ++j) v[i][j] = s.scaled(v[i][j]);
+      }
 #pragma unroll
       for (int i = 0; i < NP; ++i)
 #pragma unroll
-        for (int j = 0; j < VE; ++j) v[i][j] = unit > 0.f ? rintf(v[i][j] * inv) : 0.f;
+        for (int j = 0; j < VE; ++j) v[i][j] = s.steps(v[i][j]);
     }
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
@@ -360,14 +383,15 @@ __global__ __launch_bounds__(kThreads) void addnorm_fwd_odd_kernel(Fwd a) {
       for (int c = threadIdx.x; c < a.d; c += kThreads)
         top = Top()(top, __float_as_uint(hrow[c] * r * a.w[c]) & 0x7fffffffu);
       top = G::reduce(top, Top());
-      const float unit = __uint_as_float(top) / 127.f;
-      const float inv = unit > 0.f ? 1.f / unit : 0.f;
+      const RowScale s(top);
       if (threadIdx.x == 0) {
-        a.scale_bias[2 * row] = unit;
+        a.scale_bias[2 * row] = s.unit;
         a.scale_bias[2 * row + 1] = 0.f;
       }
-      for (int c = threadIdx.x; c < a.d; c += kThreads)
-        y[row * a.y_ld + c] = unit > 0.f ? (TY)rintf(hrow[c] * r * a.w[c] * inv) : (TY)0;
+      for (int c = threadIdx.x; c < a.d; c += kThreads) {
+        const float v = hrow[c] * r * a.w[c];
+        y[row * a.y_ld + c] = (TY)(int)s.steps(s.tiny() ? s.scaled(v) : v);
+      }
     } else {
       for (int c = threadIdx.x; c < a.d; c += kThreads) y[row * a.y_ld + c] = from_f32<TY>(hrow[c] * r * a.w[c]);
     }

@@ -472,8 +472,9 @@ int dlrm_dropout(const void* x, int64_t x_ld, void* y, int64_t y_ld, int32_t dty
  *   h        nullable, dtype: the new residual stream.  The norm takes the
  *            fp32 sum, not its rounded copy.  h may be x or res (same ld).
  *   y        y_dtype: dtype, or DLRM_I8 with scale_bias fp32 [n][2]: per
- *            row s = max |y| / 127, q = y / s rounded to nearest even,
- *            (s, 0) stored, so the rows and pairs are table rows that
+ *            row s = max |y| / 127, q = y / s rounded to nearest even (and
+ *            held to +-127, which a subnormal s may fall short of), (s, 0)
+ *            stored, so the rows and pairs are table rows that
  *            dlrm_embbag_fwd_lp reads (a row of zeros: s = 0, q = 0; a row
  *            with a NaN: s = NaN, q = 0).
  *   rstd     nullable fp32 [n], r for the backward call.

@@ -273,6 +273,29 @@ def test_add_rmsnorm_int8_special_rows(dtype):
         assert torch.equal(pooled, clean.float() * sb2[:, :1])
 
 
+@pytest.mark.parametrize("d", [64, 100, 65, 1024])
+@pytest.mark.parametrize("top", [2.0 ** 100, 1.0, 2.0 ** -112, 2.0 ** -114, 2.0 ** -121, 2.0 ** -126, 1e-40, 256 * 2.0 ** -149,
+                                 190 * 2.0 ** -149, 71 * 2.0 ** -149, 40 * 2.0 ** -149])
+def test_add_rmsnorm_int8_scales_down_to_the_smallest(d, top):
+    """Rows of +-1 have r = 1, so y = +-w exactly, down to subnormal w: s is
+    max |w| / 127 rounded once, q is w / s to the nearest step (the reciprocal
+    and the product round, 2 u32 each of at most 127 steps), at most 127."""
+    banner(f"addnorm int8 scales {d} {top}")
+    g = torch.Generator().manual_seed(d)
+    w = (torch.rand(d, generator=g, dtype=torch.float64) * top).float()
+    w[3] = top
+    x = torch.where(torch.rand(5, d, generator=g) < 0.5, -1.0, 1.0)
+    y, sb = _out(5, d, torch.int8), torch.empty((5, 2), device=DEV)
+    _D().dlrm_add_rmsnorm_fwd(x.to(DEV), d, None, 0, w.to(DEV), 5, d, 0.0, 0.0, None, None, 0, y, d, sb, None)
+    s = np.float32(w.max().numpy()) / np.float32(127)
+    assert (sb[:, 0].cpu().numpy() == s).all() and not sb[:, 1].any()
+    if s == 0:
+        assert not y.any()
+        return
+    want = (x.double() * w.double() / float(s)).clamp(-127, 127)
+    assert bool(((y.cpu().double() - want).abs() <= 0.5 + 127 * 4 * U32).all())
+
+
 @pytest.mark.parametrize("dtype", [FP, BF])
 @pytest.mark.parametrize("n,d,ld", SHAPES + [(3000, 24, 24), (2500, 128, 128)])
 @pytest.mark.parametrize("p,with_dh", [(0.0, True), (0.25, False), (0.25, True)])
