@@ -25,6 +25,7 @@ gradient of every parameter.
 from __future__ import annotations
 
 import math
+from contextlib import nullcontext
 from dataclasses import dataclass
 
 import torch
@@ -49,8 +50,16 @@ def make_layer(w, Wqkv, Wo, decay, device="cuda") -> HistoryLayer:
                         make_mlp((Wo.shape[1], Wo.shape[0]), [Wo], [zeros(Wo)], True, device), f32(decay))
 
 
+def _on(stream):
+    """A call's stream as torch's current one: the buffers that the call makes
+    are then reused in that stream's order, and the indices that torch computes
+    are ready for the kernels behind them."""
+    return nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 class HistoryTower:
-    """Parameters and call sequence; buffers are made per batch shape."""
+    """Parameters and call sequence; buffers are made per call, on its stream.
+    A batch's backward pass goes to the stream of its forward pass."""
 
     def __init__(self, table, layers, w_out, H: int, dk: int, dv: int, eps: float = 1e-6, train: bool = False,
                  p: float = 0.0):
@@ -139,28 +148,30 @@ class HistoryTower:
         longer than max_len.  Writes each history's vector (zeros for an empty
         one) to fp32 rows of ``out``, leaves the attention states in
         ``self.states``."""
-        B, n = offsets.numel() - 1, tokens.numel()
-        if n == 0:  # every history is empty: zeros, from a lookup that names no row
+        with _on(stream):
+            B, n = offsets.numel() - 1, tokens.numel()
+            state = lambda: self._empty(B, self.H, self.dk, self.dv, dtype=torch.float32)  # noqa: E731
+            if n == 0:  # every history is empty: zeros, from a lookup that names no row
+                if self.train:
+                    raise ValueError("a training batch without events")
+                self.states = [state().zero_() for _ in self.layers]
+                nobody = torch.full((B,), -1, dtype=torch.int64, device=self.table.device)
+                C.dlrm_token_embed_fwd(self.table, self.V, self.d, nobody, B, 1.0, out, out_ld, stream)
+                return out
+            self.states = [state() for _ in self.layers]
+            shape = (B, self.H, max_len, self.dk, self.dv)
+            ws = self._ws(C.dlrm_linattn_workspace_size(*shape))
+
+            def attend(i, q, k, v, o):
+                C.dlrm_linattn_fwd(q, k, v, offsets, *shape, self.layers[i].decay, self.scale, None, o, self.states[i],
+                                   ws, stream)
+
+            y = self._events(tokens, attend, stream)
+            last = torch.where(offsets[1:] > offsets[:-1], offsets[1:] - 1, -1)
+            C.dlrm_token_embed_fwd(y, n, self.d, last, B, 1.0, out, out_ld, stream)
             if self.train:
-                raise ValueError("a training batch without events")
-            self.states = [self._empty(B, self.H, self.dk, self.dv, dtype=torch.float32).zero_() for _ in self.layers]
-            nobody = torch.full((B,), -1, dtype=torch.int64, device=self.table.device)
-            C.dlrm_token_embed_fwd(self.table, self.V, self.d, nobody, B, 1.0, out, out_ld, stream)
+                self._batch = (tokens, offsets, max_len, last)
             return out
-        self.states = [self._empty(B, self.H, self.dk, self.dv, dtype=torch.float32) for _ in self.layers]
-        shape = (B, self.H, max_len, self.dk, self.dv)
-        ws = self._ws(C.dlrm_linattn_workspace_size(*shape))
-
-        def attend(i, q, k, v, o):
-            C.dlrm_linattn_fwd(q, k, v, offsets, *shape, self.layers[i].decay, self.scale, None, o, self.states[i], ws,
-                               stream)
-
-        y = self._events(tokens, attend, stream)
-        last = torch.where(offsets[1:] > offsets[:-1], offsets[1:] - 1, -1)
-        C.dlrm_token_embed_fwd(y, n, self.d, last, B, 1.0, out, out_ld, stream)
-        if self.train:
-            self._batch = (tokens, offsets, max_len, last)
-        return out
 
     def step(self, tokens, pools, slots, out=None, out_ld: int = 0, rows=None, stream=None):
         """One new event per user: tokens int64 [B], pools the layers' states
@@ -168,68 +179,72 @@ class HistoryTower:
         (distinct; -1: no user).  Writes the users' vectors to ``out`` (fp32
         rows), or with ``rows`` = (int8 [B][d], fp32 [B][2]) as int8 table rows
         and their scales and biases, which dlrm_embbag_fwd_lp reads."""
-        if self.train:
-            raise ValueError("step() is a serving call")
-        B = tokens.numel()
+        with _on(stream):
+            if self.train:
+                raise ValueError("step() is a serving call")
+            B = tokens.numel()
+            if B == 0:
+                return out if rows is None else rows
 
-        def attend(i, q, k, v, o):
-            C.dlrm_linattn_step(q, k, v, B, self.H, self.dk, self.dv, self.layers[i].decay, self.scale, pools[i], slots,
-                                o, stream)
+            def attend(i, q, k, v, o):
+                C.dlrm_linattn_step(q, k, v, B, self.H, self.dk, self.dv, self.layers[i].decay, self.scale, pools[i],
+                                    slots, o, stream)
 
-        y = self._events(tokens, attend, stream, rows)
-        if rows is None:
-            every = torch.arange(B, device=tokens.device)
-            C.dlrm_token_embed_fwd(y, B, self.d, every, B, 1.0, out, out_ld, stream)
-            return out
-        return rows
+            y = self._events(tokens, attend, stream, rows)
+            if rows is None:
+                every = torch.arange(B, device=tokens.device)
+                C.dlrm_token_embed_fwd(y, B, self.d, every, B, 1.0, out, out_ld, stream)
+                return out
+            return rows
 
     def backward(self, dout, dout_ld: int, stream=None) -> dict:
         """Gradients of the last ``forward`` (train=True) from those of its fp32
         output rows: {"table" fp32 [V][d], "w_out", "layers": [{"w", "qkv",
         "out"}]}.  Moves the dropout's offsets on, so the next forward draws
         new masks."""
-        if not self.train:
-            raise ValueError("backward() needs train=True")
-        tokens, offsets, max_len, last = self._batch
-        n, B, d, H, dk, dv = tokens.numel(), last.numel(), self.d, self.H, self.dk, self.dv
-        f32 = dict(dtype=torch.float32)
+        with _on(stream):
+            if not self.train:
+                raise ValueError("backward() needs train=True")
+            tokens, offsets, max_len, last = self._batch
+            n, B, d, H, dk, dv = tokens.numel(), last.numel(), self.d, self.H, self.dk, self.dv
+            f32 = dict(dtype=torch.float32)
 
-        def embed_bwd(tok, count, g, ld, rows, scale):
-            dT = self._empty(rows, d, **f32)
-            ws = self._ws(C.dlrm_token_embed_bwd_workspace_size(count, rows, d))
-            C.dlrm_token_embed_bwd(tok, count, g, ld, rows, d, scale, dT, False, ws, stream)
-            return dT
+            def embed_bwd(tok, count, g, ld, rows, scale):
+                dT = self._empty(rows, d, **f32)
+                ws = self._ws(C.dlrm_token_embed_bwd_workspace_size(count, rows, d))
+                C.dlrm_token_embed_bwd(tok, count, g, ld, rows, d, scale, dT, False, ws, stream)
+                return dT
 
-        def norm_bwd(i, dy, dh, h, rstd, w):
-            dx, dres, dw = self._empty(n, d), self._empty(n, d), self._empty(d, **f32)
-            ws = self._ws(C.dlrm_add_rmsnorm_bwd_workspace_size(n, d))
-            C.dlrm_add_rmsnorm_bwd(dy, d, dh, d, h, d, w, rstd, n, d, self.p, self.rng[i], dx, d, dres, d, dw, ws,
-                                   stream)
-            return dx, dres, dw
+            def norm_bwd(i, dy, dh, h, rstd, w):
+                dx, dres, dw = self._empty(n, d), self._empty(n, d), self._empty(d, **f32)
+                ws = self._ws(C.dlrm_add_rmsnorm_bwd_workspace_size(n, d))
+                C.dlrm_add_rmsnorm_bwd(dy, d, dh, d, h, d, w, rstd, n, d, self.p, self.rng[i], dx, d, dres, d, dw, ws,
+                                       stream)
+                return dx, dres, dw
 
-        def linear_bwd(mlp, kept, g):
-            k, m = mlp.dims
-            dW, db, dx = self._empty(m, k, **f32), self._empty(m, **f32), self._empty(n, k, **f32)
-            ws = self._ws(C.dlrm_mlp_bwd_workspace_size(n, mlp.dims))
-            C.dlrm_mlp_bwd(n, mlp.dims, mlp.Ws, mlp.w_ld, C.DLRM_ACT_NONE, kept[0], kept[1], m, g, m, [dW], [db], dx, k,
-                           ws, stream)
-            return dx, dW
+            def linear_bwd(mlp, kept, g):
+                k, m = mlp.dims
+                dW, db, dx = self._empty(m, k, **f32), self._empty(m, **f32), self._empty(n, k, **f32)
+                ws = self._ws(C.dlrm_mlp_bwd_workspace_size(n, mlp.dims))
+                C.dlrm_mlp_bwd(n, mlp.dims, mlp.Ws, mlp.w_ld, C.DLRM_ACT_NONE, kept[0], kept[1], m, g, m, [dW], [db],
+                               dx, k, ws, stream)
+                return dx, dW
 
-        dy = embed_bwd(last, B, dout, dout_ld, n, 1.0)
-        h, rstd = self._saved[-1]
-        dx, dres, dw = norm_bwd(len(self.layers), dy, None, h, rstd, self.w_out)
-        grads = {"w_out": dw, "layers": []}
-        shape = (B, H, max_len, dk, dv)
-        ws = self._ws(C.dlrm_linattn_bwd_workspace_size(*shape))
-        for i in reversed(range(len(self.layers))):
-            lay, (h, rstd, qkv, _, kept) = self.layers[i], self._saved[i]
-            do, dWo = linear_bwd(lay.out, kept[1], dx)
-            dqkv = self._empty(n, qkv.shape[1])
-            C.dlrm_linattn_bwd(*self._heads(qkv), do.view(n, H, dv), offsets, *shape, lay.decay, self.scale, None, None,
-                               *self._heads(dqkv), None, ws, stream)
-            dy, dWqkv = linear_bwd(lay.qkv, kept[0], dqkv)
-            dx, dres, dw = norm_bwd(i, dy, dres, h, rstd, lay.w)
-            grads["layers"].insert(0, {"w": dw, "qkv": dWqkv, "out": dWo})
-        grads["table"] = embed_bwd(tokens, n, dx, d, self.V, math.sqrt(d))
-        self.rng[:, 1] += (n * d + 7) // 8
-        return grads
+            dy = embed_bwd(last, B, dout, dout_ld, n, 1.0)
+            h, rstd = self._saved[-1]
+            dx, dres, dw = norm_bwd(len(self.layers), dy, None, h, rstd, self.w_out)
+            grads = {"w_out": dw, "layers": []}
+            shape = (B, H, max_len, dk, dv)
+            ws = self._ws(C.dlrm_linattn_bwd_workspace_size(*shape))
+            for i in reversed(range(len(self.layers))):
+                lay, (h, rstd, qkv, _, kept) = self.layers[i], self._saved[i]
+                do, dWo = linear_bwd(lay.out, kept[1], dx)
+                dqkv = self._empty(n, qkv.shape[1])
+                C.dlrm_linattn_bwd(*self._heads(qkv), do.view(n, H, dv), offsets, *shape, lay.decay, self.scale, None,
+                                   None, *self._heads(dqkv), None, ws, stream)
+                dy, dWqkv = linear_bwd(lay.qkv, kept[0], dqkv)
+                dx, dres, dw = norm_bwd(i, dy, dres, h, rstd, lay.w)
+                grads["layers"].insert(0, {"w": dw, "qkv": dWqkv, "out": dWo})
+            grads["table"] = embed_bwd(tokens, n, dx, d, self.V, math.sqrt(d))
+            self.rng[:, 1] += (n * d + 7) // 8
+            return grads

@@ -208,3 +208,34 @@ def test_tower_under_a_captured_graph():
         tw.step(t, pools(), None, torch.empty((B, D), device=DEV), D)
     for a, b in zip(live, eager):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("train", [False, True])
+def test_tower_on_another_stream(train):
+    """The same bits on a stream given to the calls while the current one is
+    still busy with other work."""
+    banner(f"history tower stream {train}")
+    params = _parameters(10)
+    tok, off = _histories(11, [70, 0, 9, 200])
+    tok, off = tok.to(DEV), off.to(DEV)
+    dout = torch.randn(4, D, generator=torch.Generator().manual_seed(1)).to(DEV)
+    busy = torch.zeros(1 << 26, device=DEV)
+
+    def run(stream):
+        tw = _tower(params, train=train)
+        out = torch.empty((4, D), device=DEV)
+        torch.cuda.synchronize()
+        for _ in range(60):
+            busy.add_(1.0)
+        tw.forward(tok, off, 200, out, D, stream=stream)
+        if train:
+            return out, tw.backward(dout, D, stream=stream), tw
+        pools, stepped = tw.states, torch.empty((4, D), device=DEV)
+        tw.step(tok[:4], pools, None, stepped, D, stream=stream)
+        return out, {"table": stepped, "w_out": pools[0]}, tw
+
+    want, got = run(None), run(torch.cuda.Stream())
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0])
+    for name in ("table", "w_out"):
+        assert torch.equal(got[1][name], want[1][name]), name
