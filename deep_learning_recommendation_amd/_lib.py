@@ -8,6 +8,7 @@ entry point raises: there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -288,6 +289,42 @@ def _addr(t) -> int | None:
     return None if t is None else t.data_ptr()
 
 
+@functools.lru_cache(maxsize=None)
+def _types():
+    """Activation types and their codes, and the two types of other arrays."""
+    import torch
+
+    return {torch.float32: DLRM_F32, torch.bfloat16: DLRM_BF16}, torch.float32, torch.int64
+
+
+def _act(first, *others) -> int:
+    """The code of the type that activation tensors share: one read as another
+    type would be read past its end."""
+    code = _types()[0].get(first.dtype)
+    if code is None:
+        raise TypeError(f"expected float32 or bfloat16, got {first.dtype}")
+    for t in others:
+        if t is not None and t.dtype != first.dtype:
+            raise TypeError(f"expected {first.dtype} as the first tensor, got {t.dtype}")
+    return code
+
+
+def _f32(t) -> int | None:
+    if t is None:
+        return None
+    if t.dtype != _types()[1]:
+        raise TypeError(f"expected float32, got {t.dtype}")
+    return t.data_ptr()
+
+
+def _i64(t) -> int | None:
+    if t is None:
+        return None
+    if t.dtype != _types()[2]:
+        raise TypeError(f"expected int64, got {t.dtype}")
+    return t.data_ptr()
+
+
 def _raw_stream(stream) -> int:
     """The hipStream_t of a torch stream, or of the current one: its handle
     straight from torch's C module where that is there (the stream object
@@ -318,7 +355,7 @@ def dlrm_token_embed_fwd(table, rows: int, d: int, tokens, n: int, scale: float,
                          stream=None) -> None:
     """out[i] = scale * table[tokens[i]]; a token outside [0, rows) gives zeros."""
     _check("dlrm_token_embed_fwd", lib().dlrm_token_embed_fwd(
-        _addr(table), _dtype_code(table), rows, d, _addr(tokens), n, scale, _addr(out), _dtype_code(out), out_ld,
+        _addr(table), _act(table), rows, d, _i64(tokens), n, scale, _addr(out), _act(out), out_ld,
         _raw_stream(stream)))
 
 
@@ -331,24 +368,27 @@ def dlrm_token_embed_bwd(tokens, n: int, dout, dout_ld: int, rows: int, d: int, 
     """The fp32 table gradient, summed by sorted tokens (added to dtable with
     ``accumulate``, else every row written)."""
     _check("dlrm_token_embed_bwd", lib().dlrm_token_embed_bwd(
-        _addr(tokens), n, _addr(dout), _dtype_code(dout), dout_ld, rows, d, scale, _addr(dtable), int(accumulate),
+        _i64(tokens), n, _addr(dout), _act(dout), dout_ld, rows, d, scale, _f32(dtable), int(accumulate),
         _addr(ws), _bytes(ws), _raw_stream(stream)))
 
 
 def dlrm_dropout(x, x_ld: int, y, y_ld: int, rows: int, cols: int, p: float, rng, stream=None) -> None:
     """y = x * mask / (1 - p); rng: device int64 [2] = (seed, offset).  The
     backward pass is the same call on the gradient."""
-    _check("dlrm_dropout", lib().dlrm_dropout(_addr(x), x_ld, _addr(y), y_ld, _dtype_code(x), rows, cols, p,
-                                              _addr(rng), _raw_stream(stream)))
+    _check("dlrm_dropout", lib().dlrm_dropout(_addr(x), x_ld, _addr(y), y_ld, _act(x, y), rows, cols, p,
+                                              _i64(rng), _raw_stream(stream)))
 
 
 def dlrm_add_rmsnorm_fwd(x, x_ld: int, res, res_ld: int, w, n: int, d: int, eps: float, p: float, rng, h, h_ld: int,
                          y, y_ld: int, scale_bias, rstd, stream=None) -> None:
     """h = res + dropout(x), y = h / rms(h) * w; an int8 y comes with
     ``scale_bias`` = fp32 [n][2] (value = scale * q + bias, bias 0)."""
+    y_code = _row_dtype_code(y)
+    if y_code != DLRM_I8:
+        _act(x, y)
     _check("dlrm_add_rmsnorm_fwd", lib().dlrm_add_rmsnorm_fwd(
-        _addr(x), x_ld, _addr(res), res_ld, _dtype_code(x), _addr(w), n, d, eps, p, _addr(rng), _addr(h), h_ld,
-        _addr(y), _row_dtype_code(y), y_ld, _addr(scale_bias), _addr(rstd), _raw_stream(stream)))
+        _addr(x), x_ld, _addr(res), res_ld, _act(x, res, h), _f32(w), n, d, eps, p, _i64(rng), _addr(h), h_ld,
+        _addr(y), y_code, y_ld, _f32(scale_bias), _f32(rstd), _raw_stream(stream)))
 
 
 def dlrm_add_rmsnorm_bwd_workspace_size(n: int, d: int) -> int:
@@ -358,8 +398,8 @@ def dlrm_add_rmsnorm_bwd_workspace_size(n: int, d: int) -> int:
 def dlrm_add_rmsnorm_bwd(dy, dy_ld: int, dh, dh_ld: int, h, h_ld: int, w, rstd, n: int, d: int, p: float, rng, dx,
                          dx_ld: int, dres, dres_ld: int, dw, ws, stream=None) -> None:
     _check("dlrm_add_rmsnorm_bwd", lib().dlrm_add_rmsnorm_bwd(
-        _addr(dy), dy_ld, _addr(dh), dh_ld, _addr(h), h_ld, _dtype_code(dy), _addr(w), _addr(rstd), n, d, p,
-        _addr(rng), _addr(dx), dx_ld, _addr(dres), dres_ld, _addr(dw), _addr(ws), _bytes(ws), _raw_stream(stream)))
+        _addr(dy), dy_ld, _addr(dh), dh_ld, _addr(h), h_ld, _act(dy, dh, h, dx, dres), _f32(w), _f32(rstd), n, d, p,
+        _i64(rng), _addr(dx), dx_ld, _addr(dres), dres_ld, _f32(dw), _addr(ws), _bytes(ws), _raw_stream(stream)))
 
 
 def dlrm_linattn_workspace_size(B: int, H: int, max_len: int, dk: int, dv: int) -> int:
@@ -371,8 +411,8 @@ def dlrm_linattn_fwd(q, k, v, offsets, B: int, H: int, max_len: int, dk: int, dv
     """Linear attention over the B histories of ``offsets``; q, k, v, o are
     [rows][heads][width] tensors (views of one projection's output will do)."""
     _check("dlrm_linattn_fwd", lib().dlrm_linattn_fwd(
-        *_heads(q), *_heads(k), *_heads(v), _dtype_code(q), _addr(offsets), B, H, max_len, dk, dv, _addr(decay), scale,
-        _addr(state0), *_heads(o), _addr(state), _addr(ws), _bytes(ws), _raw_stream(stream)))
+        *_heads(q), *_heads(k), *_heads(v), _act(q, k, v, o), _i64(offsets), B, H, max_len, dk, dv, _f32(decay), scale,
+        _f32(state0), *_heads(o), _f32(state), _addr(ws), _bytes(ws), _raw_stream(stream)))
 
 
 def dlrm_linattn_bwd_workspace_size(B: int, H: int, max_len: int, dk: int, dv: int) -> int:
@@ -382,14 +422,14 @@ def dlrm_linattn_bwd_workspace_size(B: int, H: int, max_len: int, dk: int, dv: i
 def dlrm_linattn_bwd(q, k, v, do, offsets, B: int, H: int, max_len: int, dk: int, dv: int, decay, scale: float, state0,
                      dstate, dq, dk_out, dv_out, dstate0, ws, stream=None) -> None:
     _check("dlrm_linattn_bwd", lib().dlrm_linattn_bwd(
-        *_heads(q), *_heads(k), *_heads(v), *_heads(do), _dtype_code(q), _addr(offsets), B, H, max_len, dk, dv,
-        _addr(decay), scale, _addr(state0), _addr(dstate), *_heads(dq), *_heads(dk_out), *_heads(dv_out),
-        _addr(dstate0), _addr(ws), _bytes(ws), _raw_stream(stream)))
+        *_heads(q), *_heads(k), *_heads(v), *_heads(do), _act(q, k, v, do, dq, dk_out, dv_out), _i64(offsets), B, H,
+        max_len, dk, dv, _f32(decay), scale, _f32(state0), _f32(dstate), *_heads(dq), *_heads(dk_out), *_heads(dv_out),
+        _f32(dstate0), _addr(ws), _bytes(ws), _raw_stream(stream)))
 
 
 def dlrm_linattn_step(q, k, v, B: int, H: int, dk: int, dv: int, decay, scale: float, state, slots, o,
                       stream=None) -> None:
     """One new event per user on a pool of states, updated in place."""
     _check("dlrm_linattn_step", lib().dlrm_linattn_step(
-        *_heads(q), *_heads(k), *_heads(v), _dtype_code(q), B, H, dk, dv, _addr(decay), scale, _addr(state),
-        _addr(slots), *_heads(o), _raw_stream(stream)))
+        *_heads(q), *_heads(k), *_heads(v), _act(q, k, v, o), B, H, dk, dv, _f32(decay), scale, _f32(state),
+        _i64(slots), *_heads(o), _raw_stream(stream)))

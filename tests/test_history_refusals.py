@@ -149,3 +149,47 @@ def test_bindings_want_contiguous_heads():
     with pytest.raises(ValueError):
         C._heads(t[0])
     assert ctypes.sizeof(ctypes.c_void_p) == 8
+
+
+def test_bindings_refuse_mixed_types():
+    """An array read as another type would be read past its end, so the
+    bindings compare types before the call."""
+    import torch
+
+    f, b, i = torch.zeros(2, 2, 8), torch.zeros(2, 2, 8, dtype=torch.bfloat16), torch.zeros(8, dtype=torch.int64)
+    half, short = f.half(), i.int()
+    calls = [
+        lambda: C.dlrm_token_embed_fwd(half, 2, 8, i, 2, 1.0, f, 8),
+        lambda: C.dlrm_token_embed_fwd(f, 2, 8, short, 2, 1.0, f, 8),
+        lambda: C.dlrm_token_embed_fwd(f, 2, 8, i, 2, 1.0, half, 8),
+        lambda: C.dlrm_token_embed_bwd(short, 2, f, 8, 2, 8, 1.0, f, False, f),
+        lambda: C.dlrm_token_embed_bwd(i, 2, f, 8, 2, 8, 1.0, b, False, f),
+        lambda: C.dlrm_dropout(f, 8, b, 8, 2, 8, 0.5, i),
+        lambda: C.dlrm_dropout(half, 8, half, 8, 2, 8, 0.5, i),
+        lambda: C.dlrm_dropout(f, 8, f, 8, 2, 8, 0.5, short),
+        lambda: C.dlrm_add_rmsnorm_fwd(f, 8, b, 8, f, 2, 8, 0.1, 0.0, None, None, 0, f, 8, None, None),
+        lambda: C.dlrm_add_rmsnorm_fwd(f, 8, None, 8, b, 2, 8, 0.1, 0.0, None, None, 0, f, 8, None, None),
+        lambda: C.dlrm_add_rmsnorm_fwd(f, 8, None, 8, f, 2, 8, 0.1, 0.0, None, b, 8, f, 8, None, None),
+        lambda: C.dlrm_add_rmsnorm_fwd(f, 8, None, 8, f, 2, 8, 0.1, 0.0, None, None, 0, b, 8, None, None),
+        lambda: C.dlrm_add_rmsnorm_fwd(f, 8, None, 8, f, 2, 8, 0.1, 0.0, None, None, 0, f, 8, None, b),
+        lambda: C.dlrm_add_rmsnorm_bwd(f, 8, None, 0, f, 8, f, f, 2, 8, 0.0, None, b, 8, None, 0, f, f),
+        lambda: C.dlrm_add_rmsnorm_bwd(b, 8, b, 8, f, 8, f, f, 2, 8, 0.0, None, b, 8, None, 0, f, f),
+        lambda: C.dlrm_linattn_fwd(f, b, f, i, 1, 2, 2, 8, 8, f, 1.0, None, f, None, None),
+        lambda: C.dlrm_linattn_fwd(f, f, f, short, 1, 2, 2, 8, 8, f, 1.0, None, f, None, None),
+        lambda: C.dlrm_linattn_fwd(b, b, b, i, 1, 2, 2, 8, 8, b, 1.0, None, b, None, None),
+        lambda: C.dlrm_linattn_fwd(b, b, b, i, 1, 2, 2, 8, 8, f, 1.0, b, b, None, None),
+        lambda: C.dlrm_linattn_bwd(b, b, b, b, i, 1, 2, 2, 8, 8, f, 1.0, None, None, b, f, b, None, None),
+        lambda: C.dlrm_linattn_step(f, f, f, 2, 2, 8, 8, f, 1.0, b, None, f),
+        lambda: C.dlrm_linattn_step(f, f, f, 2, 2, 8, 8, f, 1.0, f, short, f),
+        lambda: C.dlrm_linattn_step(f, f, f, 2, 2, 8, 8, f, 1.0, f, None, b),
+    ]
+    for n, call in enumerate(calls):
+        with pytest.raises(TypeError):
+            call()
+            pytest.fail(f"call {n} was not refused")
+
+
+@pytest.mark.parametrize("stride", [-8, 1 << 22])
+@pytest.mark.parametrize("which", ["qt", "kt", "vt", "ot"])
+def test_linattn_row_strides(which, stride):
+    assert C.lib().dlrm_linattn_step(*change(STEP, **{which: stride})) == INV
